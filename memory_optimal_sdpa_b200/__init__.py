@@ -10,7 +10,18 @@ fallback: if libsdpa.so is missing, importing this package fails.
     O, LSE = sdpa.decode(q, k_cache, v_cache, kv_lens)      # one row per (batch, head)
     O, LSE = sdpa.decode_gqa(q, k_cache, v_cache, kv_lens)  # query heads sharing key/value heads
     dQ, dK, dV = sdpa.bwd(q, k, v, O, dO, LSE, causal=True) # gradients of fwd
+
+The bounded decode cache (C ABI in include/sdpa_cache.h):
+
+    cache = sdpa.kv4_cache(batch, heads, n_cap, d)          # keys and values in 4 bits
+    sdpa.kv4_append(cache, k_new, v_new, kv_lens)           # quantise rows into it
+    O, LSE = sdpa.decode_kv4(q, cache, kv_lens, acc=acc)    # attend; acc sums each key's weight
+    O, LSE = sdpa.decode_acc(q, k_cache, v_cache, kv_lens, acc)  # the same over a bf16 cache
+    sdpa.fwd_acc(q, k, LSE, acc, causal=True)               # the weights of a prompt
+    keep, kv_lens = sdpa.kv4_evict(cache, acc, kv_lens, budget, recent=64)  # (evict: bf16) drop the others
+    k, v = sdpa.kv4_load(cache, kv_lens)                    # the rows as bf16
 """
+import collections
 import ctypes
 import math
 import os
@@ -45,6 +56,24 @@ lib.sdpa_bwd_workspace_size.argtypes = [_i, _i, _i]
 lib.sdpa_bwd_workspace_size.restype = _sz
 lib.sdpa_bwd.argtypes = [_vp] * 9 + [_i] * 6 + [_f, _i, _vp, _sz, _vp]
 lib.sdpa_bwd.restype = _i
+lib.sdpa_kv4_append.argtypes = [_vp] * 10 + [_i] * 5 + [_vp]
+lib.sdpa_kv4_append.restype = _i
+lib.sdpa_kv4_load.argtypes = [_vp] * 7 + [_i] * 5 + [_vp]
+lib.sdpa_kv4_load.restype = _i
+lib.sdpa_decode_kv4_workspace_size.argtypes = [_i] * 6
+lib.sdpa_decode_kv4_workspace_size.restype = _sz
+lib.sdpa_decode_kv4.argtypes = [_vp] * 10 + [_i] * 5 + [_f, _vp, _sz, _vp]
+lib.sdpa_decode_kv4.restype = _i
+lib.sdpa_decode_acc_workspace_size.argtypes = [_i] * 5
+lib.sdpa_decode_acc_workspace_size.restype = _sz
+lib.sdpa_decode_acc.argtypes = [_vp] * 8 + [_i] * 5 + [_f, _vp, _sz, _vp]
+lib.sdpa_decode_acc.restype = _i
+lib.sdpa_fwd_acc.argtypes = [_vp] * 5 + [_i] * 7 + [_f, _i, _vp]
+lib.sdpa_fwd_acc.restype = _i
+lib.sdpa_evict.argtypes = [_vp] * 9 + [_i] * 7 + [_vp]
+lib.sdpa_evict.restype = _i
+lib.sdpa_kv4_evict.argtypes = [_vp] * 13 + [_i] * 7 + [_vp]
+lib.sdpa_kv4_evict.restype = _i
 lib.sdpa_get_last_device_error.argtypes = [_vp]
 lib.sdpa_get_last_device_error.restype = _i
 lib.sdpa_status_string.argtypes = [_i]
@@ -289,6 +318,259 @@ def bwd(q, k, v, o, do, lse, causal=False, scale=None, dq=None, dk=None, dv=None
                  _ptr(dv), B, H, n_q, n_kv, d_k, d_v, float(scale), int(bool(causal)), _ptr(workspace),
                  _nbytes(workspace), _stream(stream, dev)), "sdpa_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------------------ the bounded decode cache
+Kv4Cache = collections.namedtuple("Kv4Cache", "k_codes k_scales v_codes v_scales")
+Kv4Cache.__doc__ = """Keys and values in 4 bits: codes uint8 [B,H,n_cap,d/2], scales bf16 [B,H,n_cap,d/32,2] (scale, minimum)."""
+
+
+def kv4_cache(batch, heads, n_cap, d, device=None):
+    """A zeroed 4-bit cache on `device` (default: the current CUDA device); d in {64,128}."""
+    import torch
+    if d not in (64, 128):
+        raise ValueError("d must be 64 or 128, got %r" % (d,))
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return Kv4Cache(*(torch.zeros(shape, dtype=dtype, device=device) for _ in "kv" for shape, dtype in
+                      (((batch, heads, n_cap, d // 2), torch.uint8),
+                       ((batch, heads, n_cap, d // 32, 2), torch.bfloat16))))
+
+
+def _kv4(cache, name="cache", B=None, H=None, n_cap=None, d=None):
+    """Check a Kv4Cache; returns B, H, n_cap, d and its (name, tensor) pairs."""
+    import torch
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
+        raise TypeError("%s must be a Kv4Cache, got %s" % (name, type(cache).__name__))
+    kc, ks, vc, vs = cache
+    _tensor(kc, name + ".k_codes", torch.uint8, (B, H, n_cap, None if d is None else d // 2))
+    B, H, n_cap, half = kc.shape
+    scales = (B, H, n_cap, half // 16, 2)
+    _tensor(ks, name + ".k_scales", torch.bfloat16, scales)
+    _tensor(vc, name + ".v_codes", torch.uint8, (B, H, n_cap, half))
+    _tensor(vs, name + ".v_scales", torch.bfloat16, scales)
+    return B, H, n_cap, 2 * half, tuple(zip((name + ".k_codes", name + ".k_scales", name + ".v_codes",
+                                             name + ".v_scales"), cache))
+
+
+def _both(name, a, b):
+    if (a is None) != (b is None):
+        raise ValueError("give both of %s or neither" % name)
+
+
+def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, stream=None):
+    """Quantise k, v [B,H,n_rows,d] bf16 into `cache`: row t of sequence b becomes cache row kv_lens[b] + t
+    (t < n_new[b]; all rows without n_new).  kv_lens, n_new: int32 [B] on the device; kv_lens is not
+    changed.  k_read, v_read (both or neither, shapes of k, v) receive the values the cache now stands for."""
+    import torch
+    B, H, n_cap, d, parts = _kv4(cache)
+    _tensor(k, "k", torch.bfloat16, (B, H, None, d))
+    n_rows = k.shape[2]
+    _tensor(v, "v", torch.bfloat16, (B, H, n_rows, d))
+    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    if n_new is not None:
+        _tensor(n_new, "n_new", torch.int32, (B,))
+    _both("k_read and v_read", k_read, v_read)
+    if k_read is not None:
+        _tensor(k_read, "k_read", torch.bfloat16, (B, H, n_rows, d))
+        _tensor(v_read, "v_read", torch.bfloat16, (B, H, n_rows, d))
+    dev = _device("k", k, ("v", v), ("kv_lens", kv_lens), ("n_new", n_new), ("k_read", k_read), ("v_read", v_read),
+                  *parts)
+    _check(_call(dev, lib.sdpa_kv4_append, _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(n_new), *map(_ptr, cache),
+                 _ptr(k_read), _ptr(v_read), B, H, n_rows, n_cap, d, _stream(stream, dev)), "sdpa_kv4_append")
+
+
+def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
+    """Cache rows 0 .. min(kv_lens[b], n_rows) - 1 as bf16 k, v [B,H,n_rows,d].  n_rows: that of k, v where they
+    are given, else n_cap.  Rows past a sequence's length are left as they were (zero in tensors made here)."""
+    import torch
+    B, H, n_cap, d, parts = _kv4(cache)
+    _both("k and v", k, v)
+    if k is not None:
+        _tensor(k, "k", torch.bfloat16, (B, H, n_rows, d))
+        n_rows = k.shape[2]
+        _tensor(v, "v", torch.bfloat16, (B, H, n_rows, d))
+    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    dev = _device("cache.k_codes", cache[0], *parts[1:], ("kv_lens", kv_lens), ("k", k), ("v", v))
+    n_rows = n_cap if n_rows is None else n_rows
+    if n_rows < 0:
+        raise ValueError("n_rows must not be negative, got %d" % n_rows)
+    if k is None:
+        with _on(stream):
+            k, v = (torch.zeros((B, H, n_rows, d), dtype=torch.bfloat16, device=dev) for _ in "kv")
+    _check(_call(dev, lib.sdpa_kv4_load, *map(_ptr, cache), _ptr(kv_lens), _ptr(k), _ptr(v), B, H, n_rows, n_cap, d,
+                 _stream(stream, dev)), "sdpa_kv4_load")
+    return k, v
+
+
+def _on(stream):
+    """Context in which tensors are made (and filled) on `stream` (None: the current one)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _acc_args(acc, acc_out, shape):
+    """acc, acc_out of a decode or of fwd_acc: acc_out defaults to acc (the running sum)."""
+    import torch
+    if acc is not None:
+        _tensor(acc, "acc", torch.float32, shape)
+    if acc_out is not None:
+        _tensor(acc_out, "acc_out", torch.float32, shape if acc is None else tuple(acc.shape))
+    return acc if acc_out is None else acc_out
+
+
+def _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d, parts, stream):
+    import torch
+    _tensor(q, "q", torch.bfloat16, (B, None, d))
+    H_q = q.shape[1]
+    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    if o is not None:
+        _tensor(o, "o", torch.bfloat16, (B, H_q, d))
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, (B, H_q))
+    dev = _device("q", q, ("kv_lens", kv_lens), ("o", o), ("lse", lse), *parts)
+    with _on(stream):
+        if o is None:
+            o = torch.empty((B, H_q, d), dtype=torch.bfloat16, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((B, H_q), dtype=torch.float32, device=dev)
+    return H_q, o, lse, dev
+
+
+def decode_kv4_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc=False):
+    return int(lib.sdpa_decode_kv4_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d, int(bool(with_acc))))
+
+
+def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, acc=None, acc_out=None, workspace=None,
+               stream=None):
+    """Grouped-query decode over a 4-bit cache. q [B,H_q,d] bf16, cache of H_kv heads (H_q a multiple), kv_lens int32
+    [B] on the device (0: an empty slot, O = 0 and LSE = -inf).  With acc [B,H_kv,n_cap] fp32, each cached key's
+    weights, summed over the query heads that read it, are added: acc_out = acc + weights (in place without acc_out;
+    acc_out alone starts from zero); entries past kv_lens are left as they were."""
+    B, H_kv, n_cap, d, parts = _kv4(cache)
+    acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
+    H_q, o, lse, dev = _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d,
+                                       parts + (("acc", acc), ("acc_out", acc_out)), stream)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if workspace is None:
+        with _on(stream):
+            workspace = _workspace(None, decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _check(_call(dev, lib.sdpa_decode_kv4, _ptr(q), *map(_ptr, cache), _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(acc),
+                 _ptr(acc_out), B, H_q, H_kv, n_cap, d, float(scale), _ptr(workspace), _nbytes(workspace),
+                 _stream(stream, dev)), "sdpa_decode_kv4")
+    return o, lse
+
+
+def decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d):
+    return int(lib.sdpa_decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d))
+
+
+def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse=None, want_lse=True, workspace=None,
+               stream=None):
+    """decode_gqa over a bf16 cache k, v [B,H_kv,n_cap,d] that also sums the keys' attention weights; acc, acc_out (one
+    of them at least) and empty slots as in decode_kv4."""
+    import torch
+    _tensor(k, "k", torch.bfloat16, (None, None, None, None))
+    B, H_kv, n_cap, d = k.shape
+    _tensor(v, "v", torch.bfloat16, (B, H_kv, n_cap, d))
+    if acc is None and acc_out is None:
+        raise ValueError("give acc, acc_out or both")
+    acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
+    H_q, o, lse, dev = _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d,
+                                       (("k", k), ("v", v), ("acc", acc), ("acc_out", acc_out)), stream)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if workspace is None:
+        with _on(stream):
+            workspace = _workspace(None, decode_acc_workspace_size(B, H_q, H_kv, n_cap, d), dev)
+    else:
+        workspace = _workspace(workspace, 0, dev)
+    _check(_call(dev, lib.sdpa_decode_acc, _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(acc),
+                 _ptr(acc_out), B, H_q, H_kv, n_cap, d, float(scale), _ptr(workspace), _nbytes(workspace),
+                 _stream(stream, dev)), "sdpa_decode_acc")
+    return o, lse
+
+
+def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=None):
+    """The attention weights of a prompt summed over its queries and the heads of each group. q [B,H_q,n_q,d],
+    k [B,H_kv,n_kv,d] bf16, lse [B,H_q,n_q] as fwd returned it for the same mask and scale; the last n_q queries of a
+    longer prompt may be given alone (causal is bottom-right aligned).  acc [B,H_kv,n_acc] fp32, n_acc >= n_kv:
+    acc_out = acc + weights for the n_kv keys, in place without acc_out; without both a new [B,H_kv,n_kv] tensor.
+    Returns acc_out."""
+    import torch
+    _tensor(q, "q", torch.bfloat16, (None, None, None, None))
+    B, H_q, n_q, d = q.shape
+    _tensor(k, "k", torch.bfloat16, (B, None, None, d))
+    H_kv, n_kv = k.shape[1:3]
+    _tensor(lse, "lse", torch.float32, (B, H_q, n_q))
+    acc_out = _acc_args(acc, acc_out, (B, H_kv, None))
+    dev = _device("q", q, ("k", k), ("lse", lse), ("acc", acc), ("acc_out", acc_out))
+    if acc_out is None:
+        with _on(stream):
+            acc_out = torch.empty((B, H_kv, n_kv), dtype=torch.float32, device=dev)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    _check(_call(dev, lib.sdpa_fwd_acc, _ptr(q), _ptr(k), _ptr(lse), _ptr(acc), _ptr(acc_out), B, H_q, H_kv, n_q, n_kv,
+                 acc_out.shape[2], d, float(scale), int(bool(causal)), _stream(stream, dev)), "sdpa_fwd_acc")
+    return acc_out
+
+
+def _evict_args(acc, kv_lens, budget, out_name, out, acc_out, B, H, n_cap, n_out, dev_parts, stream):
+    import torch
+    _tensor(acc, "acc", torch.float32, (B, H, n_cap))
+    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    if (out is None) != (acc_out is None):
+        raise ValueError("give %s and acc_out together, or none of them (in place)" % out_name)
+    if acc_out is not None:
+        _tensor(acc_out, "acc_out", torch.float32, (B, H, n_out))
+    name, ref = dev_parts[0]
+    dev = _device(name, ref, *dev_parts[1:], ("acc", acc), ("kv_lens", kv_lens), ("acc_out", acc_out))
+    if not 1 <= budget <= n_out:
+        raise ValueError("budget must be between 1 and the output's capacity %d, got %d" % (n_out, budget))
+    with _on(stream):
+        keep = torch.empty((B, H, budget), dtype=torch.int32, device=dev)
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    return keep, new_lens, acc if acc_out is None else acc_out, dev
+
+
+def evict(k, v, acc, kv_lens, budget, recent=0, k_out=None, v_out=None, acc_out=None, stream=None):
+    """Keep at most `budget` rows of each sequence and head of a bf16 cache k, v [B,H,n_cap,d]: the last `recent` and
+    those with the largest acc [B,H,n_cap] (the lower row where equal), in order, as rows 0, 1, ...  In place, or into
+    k_out, v_out [B,H,n_out,d] and acc_out [B,H,n_out].  acc becomes the kept rows' weights, 0 after them.  Returns
+    keep int32 [B,H,budget] (the old rows, -1 past the new length) and the new lengths int32 [B]."""
+    import torch
+    _tensor(k, "k", torch.bfloat16, (None, None, None, None))
+    B, H, n_cap, d = k.shape
+    _tensor(v, "v", torch.bfloat16, (B, H, n_cap, d))
+    _both("k_out and v_out", k_out, v_out)
+    n_out = n_cap
+    if k_out is not None:
+        _tensor(k_out, "k_out", torch.bfloat16, (B, H, None, d))
+        n_out = k_out.shape[2]
+        _tensor(v_out, "v_out", torch.bfloat16, (B, H, n_out, d))
+    budget, recent = int(budget), int(recent)
+    keep, new_lens, to, dev = _evict_args(acc, kv_lens, budget, "k_out, v_out", k_out, acc_out, B, H, n_cap, n_out,
+                                          (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)), stream)
+    k_out, v_out = (k, v) if k_out is None else (k_out, v_out)
+    _check(_call(dev, lib.sdpa_evict, _ptr(k), _ptr(v), _ptr(acc), _ptr(kv_lens), _ptr(k_out), _ptr(v_out), _ptr(to),
+                 _ptr(keep), _ptr(new_lens), B, H, n_cap, n_out, d, budget, recent, _stream(stream, dev)), "sdpa_evict")
+    return keep, new_lens
+
+
+def kv4_evict(cache, acc, kv_lens, budget, recent=0, out=None, acc_out=None, stream=None):
+    """evict for a 4-bit cache: in place, or into the cache `out` (any capacity >= budget) and acc_out."""
+    B, H, n_cap, d, parts = _kv4(cache)
+    n_out, out_parts = n_cap, ()
+    if out is not None:
+        _, _, n_out, _, out_parts = _kv4(out, "out", B, H, None, d)
+    budget, recent = int(budget), int(recent)
+    keep, new_lens, to, dev = _evict_args(acc, kv_lens, budget, "out", out, acc_out, B, H, n_cap, n_out,
+                                          parts + out_parts, stream)
+    out = cache if out is None else out
+    _check(_call(dev, lib.sdpa_kv4_evict, *map(_ptr, cache), _ptr(acc), _ptr(kv_lens), *map(_ptr, out), _ptr(to),
+                 _ptr(keep), _ptr(new_lens), B, H, n_cap, n_out, d, budget, recent, _stream(stream, dev)),
+           "sdpa_kv4_evict")
+    return keep, new_lens
 
 
 def get_last_device_error(stream=None):

@@ -14,7 +14,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
 
 def sources():
     srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))]
-    return srcs + [os.path.join(ROOT, "include", "sdpa.h")]
+    inc = os.path.join(ROOT, "include")
+    return srcs + [os.path.join(inc, f) for f in sorted(os.listdir(inc)) if f.endswith(".h")]
 
 
 def build(force=False, verbose=False, extra=()):

@@ -1,0 +1,328 @@
+// cache_api.cuh -- the C ABI of include/sdpa_cache.h: argument checks and launches (part of sdpa_api.cu's
+// translation unit, whose helpers it uses).
+#pragma once
+
+#include "sdpa_cache.h"
+#include "decode_cache.cuh"
+#include "evict.cuh"
+#include "kv4.cuh"
+#include "prompt_weights.cuh"
+
+namespace {
+
+bool cache_head_dim(int d) { return d == 64 || d == 128; }
+
+// batch, heads and batch * heads * rows within what the kernels index with 32 bits.
+bool cache_sizes_fit(long long batch, long long heads, long long rows) {
+  return batch <= 65535 && heads <= 65535 && batch * heads * rows < (1LL << 31);
+}
+
+int launched(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SDPA_OK : cuda_fail(what, e);
+}
+
+template <bool LOAD>
+int launch_kv4_rows(const sdpa::Kv4RowsParams& p, int d, cudaStream_t s) {
+  const long long slots = (long long)p.B * p.H * p.n_rows;
+  const int per_block = sdpa::KV4_THREADS / (d / 8) * sdpa::KV4_UNROLL;
+  const dim3 grid((unsigned)((slots + per_block - 1) / per_block), 2);
+  if (d == 64)
+    sdpa::sdpa_kv4_rows_kernel<64, LOAD><<<grid, sdpa::KV4_THREADS, 0, s>>>(p);
+  else
+    sdpa::sdpa_kv4_rows_kernel<128, LOAD><<<grid, sdpa::KV4_THREADS, 0, s>>>(p);
+  return launched(LOAD ? "kv4 load launch" : "kv4 append launch");
+}
+
+bool cache_arrays_aligned(const void* kc, const void* ks, const void* vc, const void* vs) {
+  return aligned16(kc) && aligned16(ks) && aligned16(vc) && aligned16(vs);
+}
+
+}  // namespace
+
+extern "C" int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens, const int* n_new, void* k_codes,
+                               void* k_scales, void* v_codes, void* v_scales, void* k_read, void* v_read, int batch,
+                               int heads, int n_rows, int n_kv_cap, int d, void* stream) {
+  if (batch < 0 || heads < 0 || n_rows < 0 || n_kv_cap < 1) return SDPA_ERR_INVALID_ARG;
+  if (!cache_head_dim(d)) return SDPA_ERR_UNSUPPORTED;
+  if (batch == 0 || heads == 0 || n_rows == 0) return SDPA_OK;
+  if (!K || !V || !kv_lens || !k_codes || !k_scales || !v_codes || !v_scales || !k_read != !v_read)
+    return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !cache_arrays_aligned(k_codes, k_scales, v_codes, v_scales) ||
+      !aligned16(k_read) || !aligned16(v_read) || !aligned4(kv_lens) || !aligned4(n_new))
+    return SDPA_ERR_MISALIGNED;
+  if (!cache_sizes_fit(batch, heads, n_rows) || !cache_sizes_fit(batch, heads, n_kv_cap)) return SDPA_ERR_UNSUPPORTED;
+  if (int e = check_device()) return e;
+  sdpa::Kv4RowsParams p = {};
+  p.cache[0] = {(uint8_t*)k_codes, (uint32_t*)k_scales};
+  p.cache[1] = {(uint8_t*)v_codes, (uint32_t*)v_scales};
+  p.rows[0] = (__nv_bfloat16*)K;
+  p.rows[1] = (__nv_bfloat16*)V;
+  p.read[0] = (__nv_bfloat16*)k_read;
+  p.read[1] = (__nv_bfloat16*)v_read;
+  p.kv_lens = kv_lens;
+  p.n_new = n_new;
+  p.B = batch;
+  p.H = heads;
+  p.n_rows = n_rows;
+  p.n_cap = n_kv_cap;
+  return launch_kv4_rows<false>(p, d, (cudaStream_t)stream);
+}
+
+extern "C" int sdpa_kv4_load(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             const int* kv_lens, void* K, void* V, int batch, int heads, int n_rows, int n_kv_cap,
+                             int d, void* stream) {
+  if (batch < 0 || heads < 0 || n_rows < 0 || n_kv_cap < 1) return SDPA_ERR_INVALID_ARG;
+  if (!cache_head_dim(d)) return SDPA_ERR_UNSUPPORTED;
+  if (batch == 0 || heads == 0 || n_rows == 0) return SDPA_OK;
+  if (!K || !V || !kv_lens || !k_codes || !k_scales || !v_codes || !v_scales) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !cache_arrays_aligned(k_codes, k_scales, v_codes, v_scales) ||
+      !aligned4(kv_lens))
+    return SDPA_ERR_MISALIGNED;
+  if (!cache_sizes_fit(batch, heads, n_rows) || !cache_sizes_fit(batch, heads, n_kv_cap)) return SDPA_ERR_UNSUPPORTED;
+  if (int e = check_device()) return e;
+  sdpa::Kv4RowsParams p = {};
+  p.cache[0] = {(uint8_t*)k_codes, (uint32_t*)k_scales};
+  p.cache[1] = {(uint8_t*)v_codes, (uint32_t*)v_scales};
+  p.rows[0] = (__nv_bfloat16*)K;
+  p.rows[1] = (__nv_bfloat16*)V;
+  p.kv_lens = kv_lens;
+  p.B = batch;
+  p.H = heads;
+  p.n_rows = n_rows;
+  p.n_cap = n_kv_cap;
+  return launch_kv4_rows<true>(p, d, (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------------ decode over a bounded cache
+namespace {
+
+// Floats: LSE (base 2) per head, one partial log-sum-exp and d outputs per (head, split), scores per (head, row).
+size_t cache_ws_bytes(long long batch, long long heads_q, long long heads_kv, long long n_cap, long long d, bool with_acc) {
+  (void)heads_kv;
+  const long long ns = (n_cap + sdpa::CACHE_CHUNK - 1) / sdpa::CACHE_CHUNK;
+  const long long floats = batch * heads_q * (1 + ns * (d + 1) + (with_acc ? n_cap : 0));
+  return ((size_t)floats * sizeof(float) + 15) / 16 * 16;
+}
+
+size_t cache_ws_size(int batch, int heads_q, int heads_kv, int n_cap, int d, bool with_acc) {
+  if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || n_cap <= 0 || !cache_head_dim(d)) return 0;
+  return cache_ws_bytes(batch, heads_q, heads_kv, n_cap, d, with_acc);
+}
+
+template <int D, bool KV4>
+int launch_cache_decode(sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
+  const int hb = (p.group + sdpa::CACHE_HEADS - 1) / sdpa::CACHE_HEADS;
+  sdpa::sdpa_cache_split_kernel<D, KV4>
+      <<<dim3((unsigned)p.n_split, (unsigned)(p.H_kv * hb), (unsigned)batch), sdpa::CACHE_THREADS, 0, s>>>(p);
+  sdpa::sdpa_cache_finish_kernel<D><<<(unsigned)(batch * p.H_q), D, 0, s>>>(p);
+  if (p.scores)
+    sdpa::sdpa_cache_weights_kernel<<<dim3((unsigned)((p.n_cap + 255) / 256), (unsigned)p.H_kv, (unsigned)batch), 256, 0, s>>>(p);
+  return launched("cache decode launch");
+}
+
+// The part that both decodes share: p holds the cache; everything else is checked and filled in here.
+int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* kv_lens, void* O, float* LSE,
+                 const float* acc, float* acc_out, int batch, int heads_q, int heads_kv, int n_cap, int d, float scale,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!aligned16(Q) || !aligned16(O) || !aligned4(kv_lens) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out))
+    return SDPA_ERR_MISALIGNED;
+  if (!cache_sizes_fit(batch, heads_q, 1) || !cache_sizes_fit(batch, heads_kv, n_cap)) return SDPA_ERR_UNSUPPORTED;
+  const size_t need = cache_ws_bytes(batch, heads_q, heads_kv, n_cap, d, acc_out != nullptr);
+  if (!workspace || workspace_bytes < need) return SDPA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return SDPA_ERR_MISALIGNED;
+  if (int e = check_device()) return e;
+  p.Q = (const __nv_bfloat16*)Q;
+  p.kv_lens = kv_lens;
+  p.acc = acc;
+  p.acc_out = acc_out;
+  p.O = (__nv_bfloat16*)O;
+  p.LSE = LSE;
+  p.H_q = heads_q;
+  p.H_kv = heads_kv;
+  p.group = heads_q / heads_kv;
+  p.n_cap = n_cap;
+  p.chunk = sdpa::CACHE_CHUNK;
+  p.n_split = (n_cap + p.chunk - 1) / p.chunk;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const size_t bh = (size_t)batch * heads_q;
+  p.part_o = (float*)workspace;
+  p.part_lse = p.part_o + bh * p.n_split * d;
+  p.lse2 = p.part_lse + bh * p.n_split;
+  p.scores = acc_out ? p.lse2 + bh : nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d == 64) return kv4 ? launch_cache_decode<64, true>(p, batch, s) : launch_cache_decode<64, false>(p, batch, s);
+  return kv4 ? launch_cache_decode<128, true>(p, batch, s) : launch_cache_decode<128, false>(p, batch, s);
+}
+
+}  // namespace
+
+extern "C" size_t sdpa_decode_kv4_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d, int with_acc) {
+  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc != 0);
+}
+
+extern "C" size_t sdpa_decode_acc_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d) {
+  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, true);
+}
+
+extern "C" int sdpa_decode_kv4(const void* Q, const void* k_codes, const void* k_scales, const void* v_codes,
+                               const void* v_scales, const int* kv_lens, void* O, float* LSE, const float* acc,
+                               float* acc_out, int batch, int heads_q, int heads_kv, int n_kv_cap, int d, float scale,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || heads_q < 0 || heads_kv < 1 || n_kv_cap < 1 || heads_q % heads_kv != 0 || !std::isfinite(scale))
+    return SDPA_ERR_INVALID_ARG;
+  if (!cache_head_dim(d)) return SDPA_ERR_UNSUPPORTED;
+  if (batch == 0 || heads_q == 0) return SDPA_OK;
+  if (!Q || !k_codes || !k_scales || !v_codes || !v_scales || !kv_lens || !O || (acc && !acc_out))
+    return SDPA_ERR_INVALID_ARG;
+  if (!cache_arrays_aligned(k_codes, k_scales, v_codes, v_scales)) return SDPA_ERR_MISALIGNED;
+  sdpa::CacheDecodeParams p = {};
+  p.cache[0] = {(uint8_t*)k_codes, (uint32_t*)k_scales};
+  p.cache[1] = {(uint8_t*)v_codes, (uint32_t*)v_scales};
+  return cache_decode(p, true, Q, kv_lens, O, LSE, acc, acc_out, batch, heads_q, heads_kv, n_kv_cap, d, scale, workspace,
+                      workspace_bytes, stream);
+}
+
+extern "C" int sdpa_decode_acc(const void* Q, const void* K, const void* V, const int* kv_lens, void* O, float* LSE,
+                               const float* acc, float* acc_out, int batch, int heads_q, int heads_kv, int n_kv_cap,
+                               int d, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (batch < 0 || heads_q < 0 || heads_kv < 1 || n_kv_cap < 1 || heads_q % heads_kv != 0 || !std::isfinite(scale))
+    return SDPA_ERR_INVALID_ARG;
+  if (!cache_head_dim(d)) return SDPA_ERR_UNSUPPORTED;
+  if (batch == 0 || heads_q == 0) return SDPA_OK;
+  if (!Q || !K || !V || !kv_lens || !O || !acc_out) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V)) return SDPA_ERR_MISALIGNED;
+  sdpa::CacheDecodeParams p = {};
+  p.rows[0] = (const __nv_bfloat16*)K;
+  p.rows[1] = (const __nv_bfloat16*)V;
+  return cache_decode(p, false, Q, kv_lens, O, LSE, acc, acc_out, batch, heads_q, heads_kv, n_kv_cap, d, scale,
+                      workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ weights of a prompt
+extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, const float* acc, float* acc_out, int batch,
+                            int heads_q, int heads_kv, int n_q, int n_kv, int n_acc, int d, float scale, int causal,
+                            void* stream) {
+  if (batch < 0 || heads_q < 0 || heads_kv < 1 || n_q < 0 || n_kv < 1 || n_acc < n_kv || (causal != 0 && causal != 1) ||
+      heads_q % heads_kv != 0 || !std::isfinite(scale))
+    return SDPA_ERR_INVALID_ARG;
+  if (!cache_head_dim(d)) return SDPA_ERR_UNSUPPORTED;
+  if (batch == 0 || heads_q == 0) return SDPA_OK;
+  if (!K || !acc_out || (n_q > 0 && (!Q || !LSE))) return SDPA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out)) return SDPA_ERR_MISALIGNED;
+  if (!cache_sizes_fit(batch, heads_q, n_q) || !cache_sizes_fit(batch, heads_kv, n_acc) ||
+      (long long)batch * heads_kv > 65535)
+    return SDPA_ERR_UNSUPPORTED;
+  if (int e = check_device()) return e;
+  sdpa::PromptWeightsParams p = {};
+  p.Q = (const __nv_bfloat16*)Q;
+  p.K = (const __nv_bfloat16*)K;
+  p.LSE = LSE;
+  p.acc = acc;
+  p.acc_out = acc_out;
+  p.H_q = heads_q;
+  p.H_kv = heads_kv;
+  p.group = heads_q / heads_kv;
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.n_acc = n_acc;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const dim3 grid((unsigned)((n_kv + 127) / 128), (unsigned)(batch * heads_kv));
+  cudaStream_t s = (cudaStream_t)stream;
+  if (d == 64)
+    sdpa::sdpa_prompt_weights_kernel<64><<<grid, 128, 0, s>>>(p);
+  else
+    sdpa::sdpa_prompt_weights_kernel<128><<<grid, 128, 0, s>>>(p);
+  return launched("prompt weights launch");
+}
+
+// ------------------------------------------------------------------ eviction
+namespace {
+
+struct EvictArray {
+  const void* in;
+  void* out;
+  size_t row_bytes;
+};
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
+// arrays[0 .. n) are the cache's rows; the weights are added here.
+int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens, float* acc_out, int* keep,
+          int* new_lens, int batch, int heads, int n_cap, int n_out, int budget, int recent, void* stream) {
+  const size_t bh = (size_t)batch * heads;
+  EvictArray all[5];
+  for (int i = 0; i < n; ++i) all[i] = arrays[i];
+  all[n] = {acc, acc_out, 4};
+  for (int i = 0; i <= n; ++i) {
+    if (!all[i].in || !all[i].out) return SDPA_ERR_INVALID_ARG;
+    if (i < n ? !aligned16(all[i].in) || !aligned16(all[i].out) : !aligned4(acc) || !aligned4(acc_out))
+      return SDPA_ERR_MISALIGNED;
+  }
+  if (!kv_lens || !keep || !new_lens) return SDPA_ERR_INVALID_ARG;
+  if (!aligned4(kv_lens) || !aligned4(keep) || !aligned4(new_lens)) return SDPA_ERR_MISALIGNED;
+  if (!cache_sizes_fit(batch, heads, n_cap) || !cache_sizes_fit(batch, heads, n_out)) return SDPA_ERR_UNSUPPORTED;
+  if (overlap(kv_lens, (size_t)batch * 4, new_lens, (size_t)batch * 4)) return SDPA_ERR_INVALID_ARG;
+  for (int i = 0; i <= n; ++i)  // an output is its own input or apart from every input and output
+    for (int j = 0; j <= n; ++j) {
+      const bool in_place = i == j && all[i].in == all[i].out && n_out == n_cap;
+      if (!in_place && overlap(all[i].out, bh * n_out * all[i].row_bytes, all[j].in, bh * n_cap * all[j].row_bytes))
+        return SDPA_ERR_INVALID_ARG;
+      if (i != j && overlap(all[i].out, bh * n_out * all[i].row_bytes, all[j].out, bh * n_out * all[j].row_bytes))
+        return SDPA_ERR_INVALID_ARG;
+    }
+  if (int e = check_device()) return e;
+  cudaStream_t s = (cudaStream_t)stream;
+  sdpa::EvictParams p = {acc, acc_out, kv_lens, keep, new_lens, heads, n_cap, n_out, budget, recent};
+  sdpa::sdpa_evict_select_kernel<<<(unsigned)bh, sdpa::EVICT_THREADS, 0, s>>>(p);
+  sdpa::EvictRowsParams r = {};
+  for (int i = 0; i < n; ++i) {
+    r.src[i] = (const uint8_t*)arrays[i].in;
+    r.dst[i] = (uint8_t*)arrays[i].out;
+    r.row_bytes[i] = (int)arrays[i].row_bytes;
+  }
+  r.keep = keep;
+  r.kv_lens = kv_lens;
+  r.n_arrays = n;
+  r.H = heads;
+  r.n_cap = n_cap;
+  r.n_out = n_out;
+  r.budget = budget;
+  sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)bh, (unsigned)n), 256, 0, s>>>(r);
+  return launched("evict launch");
+}
+
+int evict_sizes(int batch, int heads, int n_cap, int n_out, int d, int budget, int recent) {
+  if (batch < 0 || heads < 0 || n_cap < 1 || n_out < 1 || budget < 1 || budget > n_out || recent < 0 || recent > budget)
+    return SDPA_ERR_INVALID_ARG;
+  return cache_head_dim(d) ? SDPA_OK : SDPA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" int sdpa_evict(const void* K, const void* V, const float* acc, const int* kv_lens, void* K_out, void* V_out,
+                          float* acc_out, int* keep, int* new_lens, int batch, int heads, int n_kv_cap, int n_out_cap,
+                          int d, int budget, int recent, void* stream) {
+  if (int e = evict_sizes(batch, heads, n_kv_cap, n_out_cap, d, budget, recent)) return e;
+  if (batch == 0 || heads == 0) return SDPA_OK;
+  const EvictArray a[2] = {{K, K_out, (size_t)d * 2}, {V, V_out, (size_t)d * 2}};
+  return evict(a, 2, acc, kv_lens, acc_out, keep, new_lens, batch, heads, n_kv_cap, n_out_cap, budget, recent, stream);
+}
+
+extern "C" int sdpa_kv4_evict(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                              const float* acc, const int* kv_lens, void* k_codes_out, void* k_scales_out,
+                              void* v_codes_out, void* v_scales_out, float* acc_out, int* keep, int* new_lens,
+                              int batch, int heads, int n_kv_cap, int n_out_cap, int d, int budget, int recent,
+                              void* stream) {
+  if (int e = evict_sizes(batch, heads, n_kv_cap, n_out_cap, d, budget, recent)) return e;
+  if (batch == 0 || heads == 0) return SDPA_OK;
+  const size_t codes = (size_t)d / 2, scales = (size_t)d / 8;
+  const EvictArray a[4] = {{k_codes, k_codes_out, codes},
+                           {k_scales, k_scales_out, scales},
+                           {v_codes, v_codes_out, codes},
+                           {v_scales, v_scales_out, scales}};
+  return evict(a, 4, acc, kv_lens, acc_out, keep, new_lens, batch, heads, n_kv_cap, n_out_cap, budget, recent, stream);
+}

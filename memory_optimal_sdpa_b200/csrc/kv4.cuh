@@ -1,0 +1,214 @@
+// kv4.cuh -- writing rows into the 4-bit key/value cache and reading them back.
+//
+// A row's d channels form NG = d / 32 groups; group g has a scale s and a minimum m (bf16) and a 4-bit
+// code per channel, x ~ s c + m.  Byte 2 (r NG + g) + e holds channels 32 g + 4 r + 2 e (low four bits)
+// and + 1: a row is 8 chunks (r) of NG 16-bit pieces (g) of four channels.
+//
+// Both directions are streams (append: 2 d bytes in and d / 2 + d / 8 out per row, plus 2 d for the values
+// read back; load: the reverse), so a thread moves 16 bytes of bf16 with one access: eight channels
+// 32 g + 8 t .. + 7 (t = 0 .. 3), which are the pieces r = 2 t and 2 t + 1 of group g.  The four threads
+// of a group find its extremes by two shuffles.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "decode.cuh"
+#include "sm100.cuh"
+
+namespace sdpa {
+
+struct Kv4Cache {
+  uint8_t* codes;   // [B, H, n_cap, D / 2]
+  uint32_t* scales; // [B, H, n_cap, NG] (s in bits 0 .. 15, m in bits 16 .. 31)
+};
+
+struct Kv4RowsParams {
+  Kv4Cache cache[2];          // K, V
+  __nv_bfloat16* rows[2];     // [B, H, n_rows, D]
+  __nv_bfloat16* read[2];     // append: the values read back, or null
+  const int* kv_lens;         // [B]
+  const int* n_new;           // append: [B] or null
+  int B, H, n_rows, n_cap;
+};
+
+__device__ __forceinline__ float bf16_bits_to_float(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+// The smallest bf16 number (its bits) not below (hi - lo) / 15, hi >= lo finite, for hi - lo < 2^128: the
+// difference is kept exactly as the pair dh + dl (two-sum), the estimate is at most two steps low, and
+// 15 s - dh - dl has the right sign because 15 s is exact and the fused step rounds once.
+__device__ __forceinline__ uint32_t kv4_scale_bits(float lo, float hi) {
+  const float dh = hi - lo;
+  const float z = dh - hi;
+  const float dl = (hi - (dh - z)) - (lo + z);
+  uint32_t s = __float_as_uint(dh * (1.f / 15.f)) >> 16;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (fmaf(15.f, bf16_bits_to_float(s), -dh) < dl) ++s;
+  return s;
+}
+
+// round((x - lo) / s), halves to even, of the exact quotient; inv ~ 1 / s.  The estimate t is within 1e-5 of
+// the quotient; within that distance of a half the sign of x - lo - (k + 1/2) s decides, which the two-sum
+// x - lo = a + e and a fused multiply-add give exactly.
+__device__ __forceinline__ uint32_t kv4_code(float x, float lo, float s, float inv) {
+  const float a = x - lo;
+  const float t = a * inv;
+  float k = rintf(t);
+  const float half = floorf(t) + 0.5f;
+  if (fabsf(t - half) < 2e-5f) {
+    const float z = a - x;
+    const float e = (x - (a - z)) - (lo + z);
+    const float r = fmaf(-half, s, a);
+    const float below = half - 0.5f;
+    const bool up = r > -e || (r == -e && ((int)below & 1));
+    k = up ? below + 1.f : below;
+  }
+  return (uint32_t)(int)k;
+}
+
+// The eight codes of this thread's channels, and the group's scale and minimum (bits).  The four threads of
+// a group are lanes differing in bits 0 and 1.
+__device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scale_bits, uint32_t& min_bits) {
+  float x[8];
+  bf16x8_to_f32(raw, x);
+  float lo = x[0], hi = x[0], bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, x[i]);
+    hi = fmaxf(hi, x[i]);
+    bad += x[i] * 0.f;  // NaN for a NaN or an infinity
+  }
+#pragma unroll
+  for (int off = 1; off <= 2; off <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    bad += __shfl_xor_sync(0xffffffffu, bad, off);
+  }
+  if (bad != 0.f) {  // NaN: the four threads agree
+    scale_bits = min_bits = 0x7FC0u;
+    return 0u;
+  }
+  // Differences of values near the largest float would overflow: work 2^-16 smaller there.
+  const float big = fmaxf(fabsf(lo), fabsf(hi));
+  const float down = big > 0x1p120f ? 0x1p-16f : 1.f;
+  min_bits = __float_as_uint(lo) >> 16;
+  const float s_down = bf16_bits_to_float(kv4_scale_bits(lo * down, hi * down));
+  scale_bits = __float_as_uint(s_down / down) >> 16;
+  if (s_down == 0.f) return 0u;
+  // and the reciprocal of a tiny scale would: work 2^64 larger there (both factors are exact)
+  const float f = big < 0x1p-60f ? 0x1p64f : down;
+  const float s = bf16_bits_to_float(scale_bits) * f;
+  lo *= f;
+  const float inv = 1.f / s;
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) codes |= kv4_code(x[i] * f, lo, s, inv) << (4 * i);
+  return codes;
+}
+
+// A thread's eight codes are the 16-bit pieces r = 2 t (low half) and 2 t + 1 (high half) of its group; the
+// 4 NG bytes from byte 4 NG t on hold piece 2 t of every group, then piece 2 t + 1 of every group.
+// Between the threads with the same t (lanes 4 g + t, g < NG): to word g of those bytes, and back.
+template <int NG>
+__device__ __forceinline__ uint32_t kv4_to_words(uint32_t codes, int lane) {
+  const int g = (lane >> 2) & (NG - 1), base = lane & ~((NG - 1) << 2);
+  const int g0 = (2 * g) & (NG - 1);               // word g: pieces of groups g0 and g0 + 1 ...
+  const uint32_t a = __shfl_sync(0xffffffffu, codes, base | (g0 << 2));
+  const uint32_t b = __shfl_sync(0xffffffffu, codes, base | ((g0 + 1) << 2));
+  return __byte_perm(a, b, g >= NG / 2 ? 0x7632 : 0x5410);  // ... the second half of the words: pieces 2 t + 1
+}
+template <int NG>
+__device__ __forceinline__ uint32_t kv4_from_words(uint32_t word, int lane) {
+  const int g = (lane >> 2) & (NG - 1), base = lane & ~((NG - 1) << 2);
+  const uint32_t a = __shfl_sync(0xffffffffu, word, base | ((g >> 1) << 2));
+  const uint32_t b = __shfl_sync(0xffffffffu, word, base | ((NG / 2 + (g >> 1)) << 2));
+  return __byte_perm(a, b, (g & 1) ? 0x7632 : 0x5410);
+}
+
+// s c + m for eight codes, rounded to bf16 (s c is exact in fp32).
+__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale) {
+  const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xFFFF0000u);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = sm100::pack_bf16x2(fmaf(s, (float)((codes >> (8 * i)) & 15u), m),
+                              fmaf(s, (float)((codes >> (8 * i + 4)) & 15u), m));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+constexpr int KV4_THREADS = 256;
+constexpr int KV4_UNROLL = 4;  // rows a thread has in flight
+
+// Length of sequence b clamped to [0, n_cap]; anything else is recorded.
+__device__ __forceinline__ int cache_len(const int* kv_lens, int b, int n_cap) {
+  const int len = kv_lens[b];
+  if (len >= 0 && len <= n_cap) return len;
+  record_error(7 /* SDPA_ERR_DEVICE_BAD_LENGTH */);
+  return len < 0 ? 0 : n_cap;
+}
+
+// LOAD false: append.  Grid: x blocks over the B H n_rows row slots, y: K, V.
+template <int D, bool LOAD>
+__global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4RowsParams p) {
+  constexpr int NG = D / 32, TPR = D / 8;  // threads per row
+  constexpr int RPB = KV4_THREADS / TPR;   // rows per block and pass
+  const int lane = threadIdx.x & 31;
+  const int part = threadIdx.x % TPR, g = part >> 2, t = part & 3;
+  const Kv4Cache c = p.cache[blockIdx.y];
+  __nv_bfloat16* rows = p.rows[blockIdx.y];
+  const uint32_t total = (uint32_t)p.B * p.H * p.n_rows;
+  const uint32_t first = blockIdx.x * (uint32_t)(RPB * KV4_UNROLL) + threadIdx.x / TPR;
+  bool on[KV4_UNROLL];
+  size_t at[KV4_UNROLL], cache_row[KV4_UNROLL];
+#pragma unroll
+  for (int u = 0; u < KV4_UNROLL; ++u) {
+    const uint32_t slot = first + u * RPB;
+    on[u] = false;
+    if (slot < total) {
+      const uint32_t bh = slot / (uint32_t)p.n_rows, row = slot - bh * p.n_rows, b = bh / (uint32_t)p.H;
+      const int len = cache_len(p.kv_lens, b, p.n_cap);
+      int to = (int)row;
+      if (LOAD) {
+        on[u] = to < len;
+      } else {
+        const int n = p.n_new ? p.n_new[b] : p.n_rows;
+        if (n < 0 || n > p.n_rows || n > p.n_cap - len) record_error(7 /* SDPA_ERR_DEVICE_BAD_LENGTH */);
+        on[u] = to < n && to < p.n_cap - len;
+        to += len;
+      }
+      at[u] = (size_t)slot * D + 8 * part;
+      cache_row[u] = (size_t)bh * p.n_cap + to;
+    }
+  }
+  if (LOAD) {
+    uint32_t word[KV4_UNROLL], scale[KV4_UNROLL];
+#pragma unroll
+    for (int u = 0; u < KV4_UNROLL; ++u) {
+      word[u] = on[u] ? *reinterpret_cast<const uint32_t*>(c.codes + cache_row[u] * (D / 2) + 4 * (t * NG + g)) : 0u;
+      scale[u] = on[u] ? c.scales[cache_row[u] * NG + g] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < KV4_UNROLL; ++u) {
+      const uint4 v = kv4_values(kv4_from_words<NG>(word[u], lane), scale[u]);
+      if (on[u]) *reinterpret_cast<uint4*>(rows + at[u]) = v;
+    }
+  } else {
+    uint4 raw[KV4_UNROLL];
+#pragma unroll
+    for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = on[u] ? ld_nc_v4(rows + at[u]) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < KV4_UNROLL; ++u) {
+      uint32_t s, m;
+      const uint32_t codes = kv4_quantise(raw[u], s, m);
+      const uint32_t word = kv4_to_words<NG>(codes, lane);
+      if (on[u]) {
+        *reinterpret_cast<uint32_t*>(c.codes + cache_row[u] * (D / 2) + 4 * (t * NG + g)) = word;
+        if (t == 0) c.scales[cache_row[u] * NG + g] = s | (m << 16);
+        if (p.read[blockIdx.y])
+          *reinterpret_cast<uint4*>(p.read[blockIdx.y] + at[u]) = kv4_values(codes, s | (m << 16));
+      }
+    }
+  }
+}
+
+}  // namespace sdpa

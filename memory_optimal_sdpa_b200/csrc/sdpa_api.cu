@@ -671,3 +671,6 @@ extern "C" const char* sdpa_status_string(int status) {
     default: return "SDPA_UNKNOWN_STATUS";
   }
 }
+
+// ------------------------------------------------------------------ include/sdpa_cache.h
+#include "cache_api.cuh"
