@@ -97,28 +97,62 @@ extern "C" int sdpa_kv4_load(const void* k_codes, const void* k_scales, const vo
 // ------------------------------------------------------------------ decode over a bounded cache
 namespace {
 
-// Floats: LSE (base 2) per head, one partial log-sum-exp and d outputs per (head, split), scores per (head, row).
-size_t cache_ws_bytes(long long batch, long long heads_q, long long heads_kv, long long n_cap, long long d, bool with_acc) {
-  (void)heads_kv;
-  const long long ns = (n_cap + sdpa::CACHE_CHUNK - 1) / sdpa::CACHE_CHUNK;
-  const long long floats = batch * heads_q * (1 + ns * (d + 1) + (with_acc ? n_cap : 0));
-  return ((size_t)floats * sizeof(float) + 15) / 16 * 16;
+// Keys per split (a multiple of 128): the largest of 2048 .. 128 whose grid over the full cache still has
+// six CTAs per SM.
+int cache_chunk(long long units, long long n_cap) {
+  int chunk = 2048;
+  while (chunk > 128 && units * ((n_cap + chunk - 1) / chunk) < 148LL * 6) chunk >>= 1;
+  return chunk;
 }
+
+// Query heads that one CTA takes: up to 8, or up to 16 where the group has more.
+int cache_head_block(int group) { return group > 8 ? 16 : 8; }
+
+int cache_units(long long batch, int heads_q, int heads_kv) {
+  const int group = heads_q / heads_kv, block = cache_head_block(group);
+  return (int)(batch * heads_kv * ((group + block - 1) / block));
+}
+
+// Floats: one log-sum-exp (base 2) and d outputs per (head, split), and the scores per (head, row).
+long long cache_score_stride(long long n_cap) { return (n_cap + 3) / 4 * 4; }
 
 size_t cache_ws_size(int batch, int heads_q, int heads_kv, int n_cap, int d, bool with_acc) {
   if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || n_cap <= 0 || !cache_head_dim(d)) return 0;
-  return cache_ws_bytes(batch, heads_q, heads_kv, n_cap, d, with_acc);
+  const long long chunk = cache_chunk(cache_units(batch, heads_q, heads_kv), n_cap);
+  const long long ns = (n_cap + chunk - 1) / chunk;
+  const long long lse = ((long long)batch * heads_q * ns + 3) / 4 * 4;
+  return (size_t)((long long)batch * heads_q * (ns * d + (with_acc ? cache_score_stride(n_cap) : 0)) + lse) * sizeof(float);
+}
+
+template <int D, bool KV4, bool WIDE>
+int launch_cache_split(const sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
+  using Cfg = sdpa::CacheCfg<D, KV4, WIDE>;
+  auto kern = sdpa::sdpa_cache_split_kernel<D, KV4, WIDE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(max dynamic smem, cache decode)", e);
+  const int hb = (p.group + Cfg::ROWS - 1) / Cfg::ROWS;
+  kern<<<dim3((unsigned)p.n_split, (unsigned)(p.H_kv * hb), (unsigned)batch), Cfg::THREADS, Cfg::SMEM_BYTES, s>>>(p);
+  return launched("cache decode launch");
 }
 
 template <int D, bool KV4>
-int launch_cache_decode(sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
-  const int hb = (p.group + sdpa::CACHE_HEADS - 1) / sdpa::CACHE_HEADS;
-  sdpa::sdpa_cache_split_kernel<D, KV4>
-      <<<dim3((unsigned)p.n_split, (unsigned)(p.H_kv * hb), (unsigned)batch), sdpa::CACHE_THREADS, 0, s>>>(p);
-  sdpa::sdpa_cache_finish_kernel<D><<<(unsigned)(batch * p.H_q), D, 0, s>>>(p);
-  if (p.scores)
-    sdpa::sdpa_cache_weights_kernel<<<dim3((unsigned)((p.n_cap + 255) / 256), (unsigned)p.H_kv, (unsigned)batch), 256, 0, s>>>(p);
-  return launched("cache decode launch");
+int launch_cache_decode(const sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
+  const int rc = cache_head_block(p.group) == 16 ? launch_cache_split<D, KV4, true>(p, batch, s)
+                                                  : launch_cache_split<D, KV4, false>(p, batch, s);
+  if (rc != SDPA_OK) return rc;
+  // a programmatic dependent: its launch overlaps the splits' last wave, and it waits for them itself
+  cudaLaunchConfig_t cfg = {};
+  const int key_blocks = p.scores ? (p.n_cap + sdpa::CACHE_FINISH_KEYS - 1) / sdpa::CACHE_FINISH_KEYS : 0;
+  cfg.gridDim = dim3((unsigned)(p.group + key_blocks), (unsigned)p.H_kv, (unsigned)batch);
+  cfg.blockDim = dim3(sdpa::CACHE_FINISH_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sdpa::sdpa_cache_finish_kernel<D>, p);
+  return e == cudaSuccess ? SDPA_OK : cuda_fail("cache decode finish launch", e);
 }
 
 // The part that both decodes share: p holds the cache; everything else is checked and filled in here.
@@ -128,7 +162,7 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   if (!aligned16(Q) || !aligned16(O) || !aligned4(kv_lens) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out))
     return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads_q, 1) || !cache_sizes_fit(batch, heads_kv, n_cap)) return SDPA_ERR_UNSUPPORTED;
-  const size_t need = cache_ws_bytes(batch, heads_q, heads_kv, n_cap, d, acc_out != nullptr);
+  const size_t need = cache_ws_size(batch, heads_q, heads_kv, n_cap, d, acc_out != nullptr);
   if (!workspace || workspace_bytes < need) return SDPA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SDPA_ERR_MISALIGNED;
   if (int e = check_device()) return e;
@@ -142,14 +176,14 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   p.H_kv = heads_kv;
   p.group = heads_q / heads_kv;
   p.n_cap = n_cap;
-  p.chunk = sdpa::CACHE_CHUNK;
+  p.chunk = cache_chunk(cache_units(batch, heads_q, heads_kv), n_cap);
+  p.score_stride = (int)cache_score_stride(n_cap);
   p.n_split = (n_cap + p.chunk - 1) / p.chunk;
   p.scale_log2 = scale * 1.4426950408889634f;
   const size_t bh = (size_t)batch * heads_q;
   p.part_o = (float*)workspace;
-  p.part_lse = p.part_o + bh * p.n_split * d;
-  p.lse2 = p.part_lse + bh * p.n_split;
-  p.scores = acc_out ? p.lse2 + bh : nullptr;
+  p.scores = acc_out ? p.part_o + bh * p.n_split * d : nullptr;  // 16-byte rows: the stride is a multiple of 4
+  p.part_lse = p.part_o + bh * (p.n_split * (size_t)d + (acc_out ? (size_t)p.score_stride : 0));
   cudaStream_t s = (cudaStream_t)stream;
   if (d == 64) return kv4 ? launch_cache_decode<64, true>(p, batch, s) : launch_cache_decode<64, false>(p, batch, s);
   return kv4 ? launch_cache_decode<128, true>(p, batch, s) : launch_cache_decode<128, false>(p, batch, s);
