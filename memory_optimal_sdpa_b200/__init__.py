@@ -321,6 +321,8 @@ def bwd(q, k, v, o, do, lse, causal=False, scale=None, dq=None, dk=None, dv=None
 
 
 # ------------------------------------------------------------------------------ the bounded decode cache
+# A decode step makes several of these calls, each a few microseconds on the GPU, so their checks take the short
+# way where everything fits: one comparison per tensor, and no context managers on the current device and stream.
 Kv4Cache = collections.namedtuple("Kv4Cache", "k_codes k_scales v_codes v_scales")
 Kv4Cache.__doc__ = """Keys and values in 4 bits: codes uint8 [B,H,n_cap,d/2], scales bf16 [B,H,n_cap,d/32,2] (scale, minimum)."""
 
@@ -336,20 +338,28 @@ def kv4_cache(batch, heads, n_cap, d, device=None):
                        ((batch, heads, n_cap, d // 32, 2), torch.bfloat16))))
 
 
-def _kv4(cache, name="cache", B=None, H=None, n_cap=None, d=None):
+def _fit(t, name, dtype, shape):
+    """_tensor for a shape without free entries."""
+    if getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous():
+        return t
+    return _tensor(t, name, dtype, shape)
+
+
+def _kv4(cache, name="cache", B=None, H=None, d=None):
     """Check a Kv4Cache; returns B, H, n_cap, d and its (name, tensor) pairs."""
     import torch
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise TypeError("%s must be a Kv4Cache, got %s" % (name, type(cache).__name__))
     kc, ks, vc, vs = cache
-    _tensor(kc, name + ".k_codes", torch.uint8, (B, H, n_cap, None if d is None else d // 2))
-    B, H, n_cap, half = kc.shape
+    _tensor(kc, name + ".k_codes", torch.uint8, (B, H, None, None if d is None else d // 2))
+    codes = kc.shape
+    B, H, n_cap, half = codes
     scales = (B, H, n_cap, half // 16, 2)
-    _tensor(ks, name + ".k_scales", torch.bfloat16, scales)
-    _tensor(vc, name + ".v_codes", torch.uint8, (B, H, n_cap, half))
-    _tensor(vs, name + ".v_scales", torch.bfloat16, scales)
-    return B, H, n_cap, 2 * half, tuple(zip((name + ".k_codes", name + ".k_scales", name + ".v_codes",
-                                             name + ".v_scales"), cache))
+    _fit(ks, name + ".k_scales", torch.bfloat16, scales)
+    _fit(vc, name + ".v_codes", torch.uint8, codes)
+    _fit(vs, name + ".v_scales", torch.bfloat16, scales)
+    return B, H, n_cap, 2 * half, ((name + ".k_codes", kc), (name + ".k_scales", ks), (name + ".v_codes", vc),
+                                   (name + ".v_scales", vs))
 
 
 def _both(name, a, b):
@@ -357,56 +367,78 @@ def _both(name, a, b):
         raise ValueError("give both of %s or neither" % name)
 
 
+def _made(stream, make):
+    """make() with its tensors made (and filled) on `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(where, dev, stream, *args):
+    """Call the library function `where` with these arguments and the stream, `dev` being current."""
+    import torch
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = _stream(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib, where)(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, where)(*args, handle)
+    _check(status, where)
+
+
 def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, stream=None):
     """Quantise k, v [B,H,n_rows,d] bf16 into `cache`: row t of sequence b becomes cache row kv_lens[b] + t
     (t < n_new[b]; all rows without n_new).  kv_lens, n_new: int32 [B] on the device; kv_lens is not
     changed.  k_read, v_read (both or neither, shapes of k, v) receive the values the cache now stands for."""
     import torch
+    bf, i32 = torch.bfloat16, torch.int32
     B, H, n_cap, d, parts = _kv4(cache)
-    _tensor(k, "k", torch.bfloat16, (B, H, None, d))
-    n_rows = k.shape[2]
-    _tensor(v, "v", torch.bfloat16, (B, H, n_rows, d))
-    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    _tensor(k, "k", bf, (B, H, None, d))
+    rows = k.shape
+    _fit(v, "v", bf, rows)
+    _fit(kv_lens, "kv_lens", i32, (B,))
     if n_new is not None:
-        _tensor(n_new, "n_new", torch.int32, (B,))
+        _fit(n_new, "n_new", i32, (B,))
     _both("k_read and v_read", k_read, v_read)
     if k_read is not None:
-        _tensor(k_read, "k_read", torch.bfloat16, (B, H, n_rows, d))
-        _tensor(v_read, "v_read", torch.bfloat16, (B, H, n_rows, d))
+        _fit(k_read, "k_read", bf, rows)
+        _fit(v_read, "v_read", bf, rows)
     dev = _device("k", k, ("v", v), ("kv_lens", kv_lens), ("n_new", n_new), ("k_read", k_read), ("v_read", v_read),
                   *parts)
-    _check(_call(dev, lib.sdpa_kv4_append, _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(n_new), *map(_ptr, cache),
-                 _ptr(k_read), _ptr(v_read), B, H, n_rows, n_cap, d, _stream(stream, dev)), "sdpa_kv4_append")
+    _launch("sdpa_kv4_append", dev, stream, _at(k), _at(v), _at(kv_lens), _at(n_new), *map(_at, cache), _at(k_read),
+            _at(v_read), B, H, rows[2], n_cap, d)
 
 
 def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
     """Cache rows 0 .. min(kv_lens[b], n_rows) - 1 as bf16 k, v [B,H,n_rows,d].  n_rows: that of k, v where they
     are given, else n_cap.  Rows past a sequence's length are left as they were (zero in tensors made here)."""
     import torch
+    bf = torch.bfloat16
     B, H, n_cap, d, parts = _kv4(cache)
     _both("k and v", k, v)
     if k is not None:
-        _tensor(k, "k", torch.bfloat16, (B, H, n_rows, d))
+        _tensor(k, "k", bf, (B, H, n_rows, d))
         n_rows = k.shape[2]
-        _tensor(v, "v", torch.bfloat16, (B, H, n_rows, d))
-    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+        _fit(v, "v", bf, (B, H, n_rows, d))
+    _fit(kv_lens, "kv_lens", torch.int32, (B,))
     dev = _device("cache.k_codes", cache[0], *parts[1:], ("kv_lens", kv_lens), ("k", k), ("v", v))
     n_rows = n_cap if n_rows is None else n_rows
     if n_rows < 0:
         raise ValueError("n_rows must not be negative, got %d" % n_rows)
     if k is None:
-        with _on(stream):
-            k, v = (torch.zeros((B, H, n_rows, d), dtype=torch.bfloat16, device=dev) for _ in "kv")
-    _check(_call(dev, lib.sdpa_kv4_load, *map(_ptr, cache), _ptr(kv_lens), _ptr(k), _ptr(v), B, H, n_rows, n_cap, d,
-                 _stream(stream, dev)), "sdpa_kv4_load")
+        k, v = _made(stream, lambda: [torch.zeros((B, H, n_rows, d), dtype=bf, device=dev) for _ in "kv"])
+    _launch("sdpa_kv4_load", dev, stream, *map(_at, cache), _at(kv_lens), _at(k), _at(v), B, H, n_rows, n_cap, d)
     return k, v
-
-
-def _on(stream):
-    """Context in which tensors are made (and filled) on `stream` (None: the current one)."""
-    import contextlib
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _acc_args(acc, acc_out, shape):
@@ -419,22 +451,30 @@ def _acc_args(acc, acc_out, shape):
     return acc if acc_out is None else acc_out
 
 
-def _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d, parts, stream):
+def _decode_run(where, size, q, keys, parts, kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
+                workspace, stream):
+    """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size` the workspace's bytes for
+    a number of query heads."""
     import torch
     _tensor(q, "q", torch.bfloat16, (B, None, d))
     H_q = q.shape[1]
-    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
+    _fit(kv_lens, "kv_lens", torch.int32, (B,))
     if o is not None:
-        _tensor(o, "o", torch.bfloat16, (B, H_q, d))
+        _fit(o, "o", torch.bfloat16, q.shape)
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, (B, H_q))
-    dev = _device("q", q, ("kv_lens", kv_lens), ("o", o), ("lse", lse), *parts)
-    with _on(stream):
-        if o is None:
-            o = torch.empty((B, H_q, d), dtype=torch.bfloat16, device=dev)
-        if lse is None and want_lse:
-            lse = torch.empty((B, H_q), dtype=torch.float32, device=dev)
-    return H_q, o, lse, dev
+        _fit(lse, "lse", torch.float32, (B, H_q))
+    dev = _device("q", q, ("kv_lens", kv_lens), ("o", o), ("lse", lse), ("acc", acc), ("acc_out", acc_out), *parts)
+
+    def outputs():
+        return (torch.empty_like(q) if o is None else o,
+                torch.empty((B, H_q), dtype=torch.float32, device=dev) if lse is None and want_lse else lse,
+                torch.empty(max(size(H_q), 16), dtype=torch.uint8, device=dev) if workspace is None
+                else _workspace(workspace, 0, dev))
+    o, lse, ws = _made(stream, outputs)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _launch(where, dev, stream, _at(q), *map(_at, keys), _at(kv_lens), _at(o), _at(lse), _at(acc), _at(acc_out), B, H_q,
+            H_kv, n_cap, d, scale, _at(ws), _nbytes(ws))
+    return o, lse
 
 
 def decode_kv4_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc=False):
@@ -449,18 +489,9 @@ def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, a
     acc_out alone starts from zero); entries past kv_lens are left as they were."""
     B, H_kv, n_cap, d, parts = _kv4(cache)
     acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    H_q, o, lse, dev = _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d,
-                                       parts + (("acc", acc), ("acc_out", acc_out)), stream)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if workspace is None:
-        with _on(stream):
-            workspace = _workspace(None, decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), dev)
-    else:
-        workspace = _workspace(workspace, 0, dev)
-    _check(_call(dev, lib.sdpa_decode_kv4, _ptr(q), *map(_ptr, cache), _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(acc),
-                 _ptr(acc_out), B, H_q, H_kv, n_cap, d, float(scale), _ptr(workspace), _nbytes(workspace),
-                 _stream(stream, dev)), "sdpa_decode_kv4")
-    return o, lse
+    return _decode_run("sdpa_decode_kv4",
+                       lambda H_q: decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), q, cache, parts,
+                       kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
 
 
 def decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d):
@@ -474,22 +505,13 @@ def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse
     import torch
     _tensor(k, "k", torch.bfloat16, (None, None, None, None))
     B, H_kv, n_cap, d = k.shape
-    _tensor(v, "v", torch.bfloat16, (B, H_kv, n_cap, d))
+    _fit(v, "v", torch.bfloat16, k.shape)
     if acc is None and acc_out is None:
         raise ValueError("give acc, acc_out or both")
     acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    H_q, o, lse, dev = _decode_outputs(q, kv_lens, o, lse, want_lse, B, H_kv, d,
-                                       (("k", k), ("v", v), ("acc", acc), ("acc_out", acc_out)), stream)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if workspace is None:
-        with _on(stream):
-            workspace = _workspace(None, decode_acc_workspace_size(B, H_q, H_kv, n_cap, d), dev)
-    else:
-        workspace = _workspace(workspace, 0, dev)
-    _check(_call(dev, lib.sdpa_decode_acc, _ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(acc),
-                 _ptr(acc_out), B, H_q, H_kv, n_cap, d, float(scale), _ptr(workspace), _nbytes(workspace),
-                 _stream(stream, dev)), "sdpa_decode_acc")
-    return o, lse
+    return _decode_run("sdpa_decode_acc", lambda H_q: decode_acc_workspace_size(B, H_q, H_kv, n_cap, d), q, (k, v),
+                       (("k", k), ("v", v)), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
+                       workspace, stream)
 
 
 def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=None):
@@ -503,34 +525,37 @@ def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=
     B, H_q, n_q, d = q.shape
     _tensor(k, "k", torch.bfloat16, (B, None, None, d))
     H_kv, n_kv = k.shape[1:3]
-    _tensor(lse, "lse", torch.float32, (B, H_q, n_q))
+    _fit(lse, "lse", torch.float32, (B, H_q, n_q))
     acc_out = _acc_args(acc, acc_out, (B, H_kv, None))
     dev = _device("q", q, ("k", k), ("lse", lse), ("acc", acc), ("acc_out", acc_out))
     if acc_out is None:
-        with _on(stream):
-            acc_out = torch.empty((B, H_kv, n_kv), dtype=torch.float32, device=dev)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    _check(_call(dev, lib.sdpa_fwd_acc, _ptr(q), _ptr(k), _ptr(lse), _ptr(acc), _ptr(acc_out), B, H_q, H_kv, n_q, n_kv,
-                 acc_out.shape[2], d, float(scale), int(bool(causal)), _stream(stream, dev)), "sdpa_fwd_acc")
+        acc_out = _made(stream, lambda: torch.empty((B, H_kv, n_kv), dtype=torch.float32, device=dev))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _launch("sdpa_fwd_acc", dev, stream, _at(q), _at(k), _at(lse), _at(acc), _at(acc_out), B, H_q, H_kv, n_q, n_kv,
+            acc_out.shape[2], d, scale, int(bool(causal)))
     return acc_out
 
 
-def _evict_args(acc, kv_lens, budget, out_name, out, acc_out, B, H, n_cap, n_out, dev_parts, stream):
+def _evict_run(where, arrays, outs, in_parts, out_parts, out_name, acc, kv_lens, budget, recent, acc_out, B, H, n_cap,
+               n_out, d, stream):
+    """The part that evict and kv4_evict share; outs None: in place."""
     import torch
-    _tensor(acc, "acc", torch.float32, (B, H, n_cap))
-    _tensor(kv_lens, "kv_lens", torch.int32, (B,))
-    if (out is None) != (acc_out is None):
+    budget, recent = int(budget), int(recent)
+    _fit(acc, "acc", torch.float32, (B, H, n_cap))
+    _fit(kv_lens, "kv_lens", torch.int32, (B,))
+    if (outs is None) != (acc_out is None):
         raise ValueError("give %s and acc_out together, or none of them (in place)" % out_name)
     if acc_out is not None:
-        _tensor(acc_out, "acc_out", torch.float32, (B, H, n_out))
-    name, ref = dev_parts[0]
-    dev = _device(name, ref, *dev_parts[1:], ("acc", acc), ("kv_lens", kv_lens), ("acc_out", acc_out))
+        _fit(acc_out, "acc_out", torch.float32, (B, H, n_out))
+    name, ref = in_parts[0]
+    dev = _device(name, ref, *in_parts[1:], *out_parts, ("acc", acc), ("kv_lens", kv_lens), ("acc_out", acc_out))
     if not 1 <= budget <= n_out:
         raise ValueError("budget must be between 1 and the output's capacity %d, got %d" % (n_out, budget))
-    with _on(stream):
-        keep = torch.empty((B, H, budget), dtype=torch.int32, device=dev)
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    return keep, new_lens, acc if acc_out is None else acc_out, dev
+    keep, new_lens = _made(stream, lambda: (torch.empty((B, H, budget), dtype=torch.int32, device=dev),
+                                            torch.empty((B,), dtype=torch.int32, device=dev)))
+    _launch(where, dev, stream, *map(_at, arrays), _at(acc), _at(kv_lens), *map(_at, arrays if outs is None else outs),
+            _at(acc if acc_out is None else acc_out), _at(keep), _at(new_lens), B, H, n_cap, n_out, d, budget, recent)
+    return keep, new_lens
 
 
 def evict(k, v, acc, kv_lens, budget, recent=0, k_out=None, v_out=None, acc_out=None, stream=None):
@@ -539,22 +564,18 @@ def evict(k, v, acc, kv_lens, budget, recent=0, k_out=None, v_out=None, acc_out=
     k_out, v_out [B,H,n_out,d] and acc_out [B,H,n_out].  acc becomes the kept rows' weights, 0 after them.  Returns
     keep int32 [B,H,budget] (the old rows, -1 past the new length) and the new lengths int32 [B]."""
     import torch
-    _tensor(k, "k", torch.bfloat16, (None, None, None, None))
+    bf = torch.bfloat16
+    _tensor(k, "k", bf, (None, None, None, None))
     B, H, n_cap, d = k.shape
-    _tensor(v, "v", torch.bfloat16, (B, H, n_cap, d))
+    _fit(v, "v", bf, k.shape)
     _both("k_out and v_out", k_out, v_out)
-    n_out = n_cap
+    n_out, outs, out_parts = n_cap, None, ()
     if k_out is not None:
-        _tensor(k_out, "k_out", torch.bfloat16, (B, H, None, d))
-        n_out = k_out.shape[2]
-        _tensor(v_out, "v_out", torch.bfloat16, (B, H, n_out, d))
-    budget, recent = int(budget), int(recent)
-    keep, new_lens, to, dev = _evict_args(acc, kv_lens, budget, "k_out, v_out", k_out, acc_out, B, H, n_cap, n_out,
-                                          (("k", k), ("v", v), ("k_out", k_out), ("v_out", v_out)), stream)
-    k_out, v_out = (k, v) if k_out is None else (k_out, v_out)
-    _check(_call(dev, lib.sdpa_evict, _ptr(k), _ptr(v), _ptr(acc), _ptr(kv_lens), _ptr(k_out), _ptr(v_out), _ptr(to),
-                 _ptr(keep), _ptr(new_lens), B, H, n_cap, n_out, d, budget, recent, _stream(stream, dev)), "sdpa_evict")
-    return keep, new_lens
+        _tensor(k_out, "k_out", bf, (B, H, None, d))
+        n_out, outs, out_parts = k_out.shape[2], (k_out, v_out), (("k_out", k_out), ("v_out", v_out))
+        _fit(v_out, "v_out", bf, k_out.shape)
+    return _evict_run("sdpa_evict", (k, v), outs, (("k", k), ("v", v)), out_parts, "k_out, v_out", acc, kv_lens, budget,
+                      recent, acc_out, B, H, n_cap, n_out, d, stream)
 
 
 def kv4_evict(cache, acc, kv_lens, budget, recent=0, out=None, acc_out=None, stream=None):
@@ -562,15 +583,9 @@ def kv4_evict(cache, acc, kv_lens, budget, recent=0, out=None, acc_out=None, str
     B, H, n_cap, d, parts = _kv4(cache)
     n_out, out_parts = n_cap, ()
     if out is not None:
-        _, _, n_out, _, out_parts = _kv4(out, "out", B, H, None, d)
-    budget, recent = int(budget), int(recent)
-    keep, new_lens, to, dev = _evict_args(acc, kv_lens, budget, "out", out, acc_out, B, H, n_cap, n_out,
-                                          parts + out_parts, stream)
-    out = cache if out is None else out
-    _check(_call(dev, lib.sdpa_kv4_evict, *map(_ptr, cache), _ptr(acc), _ptr(kv_lens), *map(_ptr, out), _ptr(to),
-                 _ptr(keep), _ptr(new_lens), B, H, n_cap, n_out, d, budget, recent, _stream(stream, dev)),
-           "sdpa_kv4_evict")
-    return keep, new_lens
+        _, _, n_out, _, out_parts = _kv4(out, "out", B, H, d)
+    return _evict_run("sdpa_kv4_evict", cache, out, parts, out_parts, "out", acc, kv_lens, budget, recent, acc_out, B, H,
+                      n_cap, n_out, d, stream)
 
 
 def get_last_device_error(stream=None):

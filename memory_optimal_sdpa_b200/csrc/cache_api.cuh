@@ -2,6 +2,8 @@
 // translation unit, whose helpers it uses).
 #pragma once
 
+#include <atomic>
+
 #include "sdpa_cache.h"
 #include "decode_cache.cuh"
 #include "evict.cuh"
@@ -32,6 +34,19 @@ int launch_kv4_rows(const sdpa::Kv4RowsParams& p, int d, cudaStream_t s) {
   else
     sdpa::sdpa_kv4_rows_kernel<128, LOAD><<<grid, sdpa::KV4_THREADS, 0, s>>>(p);
   return launched(LOAD ? "kv4 load launch" : "kv4 append launch");
+}
+
+// Allow `kern` this much dynamic shared memory on the current device, once per device (a bit of `ready` each).
+template <class Kernel>
+int allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (e == cudaSuccess && dev < 64 && (ready.load(std::memory_order_acquire) & bit)) return SDPA_OK;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(max dynamic smem, cache)", e);
+  ready.fetch_or(bit, std::memory_order_release);
+  return SDPA_OK;
 }
 
 bool cache_arrays_aligned(const void* kc, const void* ks, const void* vc, const void* vs) {
@@ -128,8 +143,8 @@ template <int D, bool KV4, bool WIDE>
 int launch_cache_split(const sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
   using Cfg = sdpa::CacheCfg<D, KV4, WIDE>;
   auto kern = sdpa::sdpa_cache_split_kernel<D, KV4, WIDE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
-  if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(max dynamic smem, cache decode)", e);
+  static std::atomic<uint64_t> ready{0};
+  if (int e = allow_smem(kern, Cfg::SMEM_BYTES, ready)) return e;
   const int hb = (p.group + Cfg::ROWS - 1) / Cfg::ROWS;
   kern<<<dim3((unsigned)p.n_split, (unsigned)(p.H_kv * hb), (unsigned)batch), Cfg::THREADS, Cfg::SMEM_BYTES, s>>>(p);
   return launched("cache decode launch");

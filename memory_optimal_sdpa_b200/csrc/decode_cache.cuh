@@ -24,6 +24,9 @@
 // two that keeps it in range; the sums with m and everything else stay in fp32.
 // bf16 caches use the same kernel with bf16 products; there p is split in two bf16 parts (its rounding to one
 // would cost as much again as that of O).
+// Both products put the cache on the MMA's side of 16 rows (keys, then channels) and the heads on its side of 8, so
+// eight heads fill it: S^T = K Q^T, O^T += V^T P^T.  The pairs p s of S^T are turned into the second product's
+// operand by an 8 x 8 transpose of the warp (movmatrix).
 //
 // Each warp streams tiles of its own (cp.async, two or three tiles in flight, no barrier between warps) with an
 // online softmax of its own; the four warps of a CTA are joined at its end.  The softmax reference moves
@@ -67,12 +70,16 @@ struct CacheCfg {
   static constexpr int NG = D / 32;
   static constexpr int SCALE_BYTES = KV4 ? 4 * TILE * NG * 4 : 0;  // s and m of K and V, as fp32
   static constexpr int WARP_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES;
-  static constexpr int JOIN_BYTES = (ROWS * D + 2 * ROWS) * 4;  // a warp's O, m, l (over the stages)
+  static constexpr int STATS = KV4 ? 2 + NG : 2;                    // m, l and the sums with the minima
+  static constexpr int JOIN_BYTES = ROWS * (D + STATS) * 4;         // a warp's results (over the stages)
   static constexpr int SMEM_BYTES = WARPS * (WARP_BYTES > JOIN_BYTES ? WARP_BYTES : JOIN_BYTES);
   static constexpr int MIN_BLOCKS = WIDE ? 2 : (KV4 ? 3 : 2);
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -95,6 +102,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A B alone (C = 0), fp16.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// A B alone, m16n8k8, tf32 operands.
+__device__ __forceinline__ void mma1688_tf32_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+
 template <bool TRANS>
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   if constexpr (TRANS)
@@ -105,6 +132,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// The 8 x 8 matrix of 16-bit elements of which a thread holds row lane / 4, columns 2 (lane % 4) and + 1, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -130,21 +163,37 @@ __device__ __forceinline__ uint4 lds<uint4>(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void sts128(uint32_t addr, float x, float y, float z, float w) {
-  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+template <int N>
+__device__ __forceinline__ void sts_row(uint32_t addr, const float* x) {
+  if constexpr (N == 4)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]) : "memory");
+  else
+    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x[0]), "f"(x[1]) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void lds_row(uint32_t addr, float (&x)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = lds<uint4>(addr);
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  } else {
+    const uint2 v = lds<uint2>(addr);
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  }
 }
 // 2^e as a float, e clamped to the normal range.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
 // ------------------------------------------------------------------------------------------ operands
-// A fragments of Q.  4-bit: per group g and step st (channels i = 2 st, 2 st + 1 of the pieces), the pairs
-// (32 g + 8 t + i, 32 g + 8 t + 4 + i), those of odd i divided by 16; see the file's head.
+// Q as the B operand (column: head 8 x + r).  4-bit: per group g and step st (channels i = 2 st, 2 st + 1 of the
+// pieces), the pairs (32 g + 8 t + i, 32 g + 8 t + 4 + i), those of odd i divided by 16; see the file's head.
 template <int D, bool KV4, bool WIDE>
 struct CacheQuery {
   static constexpr int NG = D / 32, NR = WIDE ? 2 : 1;
-  uint32_t a[D / 16][2 * NR];  // a0, a2 (row r), then a1, a3 (row r + 8)
-  float sum[NR][KV4 ? NG : 1]; // group sums of the normalised q, times 2^-24
-  float norm[NR];              // what scores are multiplied by at the end (a power of two)
+  uint32_t b[NR][D / 16][2];
+  // 4-bit: the group sums of the normalised q, times 2^-24, as two tf32 parts: the B operand (k = t, k = t + 4) of the
+  // product with the minima.  d = 128: parts 0 and 1 of group t; d = 64: part t / 2 of group t mod 2, and 0.
+  uint32_t sum[NR][2];
+  float norm[NR];  // what this head's scores are multiplied by at the end (a power of two)
 
   __device__ __forceinline__ void load(const __nv_bfloat16* q, int heads, int lane) {
     const int r = lane >> 2, t = lane & 3;
@@ -170,7 +219,7 @@ struct CacheQuery {
         if (e < -124) norm[x] = 0x1p-126f * exp2_int(e + 124);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float total = 0.f;
+          float total = 0.f;  // over the 32 channels
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             f[g][i] = f[g][i] * up * up2;
@@ -178,25 +227,29 @@ struct CacheQuery {
           }
           total += __shfl_xor_sync(0xffffffffu, total, 1);
           total += __shfl_xor_sync(0xffffffffu, total, 2);
-          sum[x][g] = total * 0x1p-24f;
+          total *= 0x1p-24f;
+          const uint32_t part0 = to_tf32(total), part1 = to_tf32(total - __uint_as_float(part0));
+          if (NG == 4) {
+            if (t == g) sum[x][0] = part0, sum[x][1] = part1;
+          } else if ((t & 1) == g) {
+            sum[x][0] = t < 2 ? part0 : part1, sum[x][1] = 0u;
+          }
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            a[2 * g + st][2 * x] = pack_f16x2(f[g][2 * st], f[g][4 + 2 * st]);
-            a[2 * g + st][2 * x + 1] = pack_f16x2(f[g][2 * st + 1] * 0.0625f, f[g][5 + 2 * st] * 0.0625f);
+            b[x][2 * g + st][0] = pack_f16x2(f[g][2 * st], f[g][4 + 2 * st]);
+            b[x][2 * g + st][1] = pack_f16x2(f[g][2 * st + 1] * 0.0625f, f[g][5 + 2 * st] * 0.0625f);
           }
         }
       } else {
         norm[x] = 1.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          a[k][2 * x] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t) : 0u;
-          a[k][2 * x + 1] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8 + 2 * t) : 0u;
+          b[x][k][0] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t) : 0u;
+          b[x][k][1] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8 + 2 * t) : 0u;
         }
       }
     }
   }
-  __device__ __forceinline__ uint32_t a1(int k) const { return WIDE ? a[k][2 * (NR - 1)] : 0u; }
-  __device__ __forceinline__ uint32_t a3(int k) const { return WIDE ? a[k][2 * (NR - 1) + 1] : 0u; }
 };
 
 // Shared-memory place (byte) of 16-byte granule gi of a K or V tile, swizzled so that the reads below meet
@@ -217,8 +270,8 @@ template <int D, bool KV4, bool WIDE>
 __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, KV4, WIDE>::MIN_BLOCKS)
     sdpa_cache_split_kernel(const CacheDecodeParams p) {
   using C = CacheCfg<D, KV4, WIDE>;
-  constexpr int NG = C::NG, NR = WIDE ? 2 : 1, NT = C::TILE / 8;  // NT: 8-key tiles of scores
-  constexpr int CG = D / 8;                                        // 8-channel tiles of outputs
+  constexpr int NG = C::NG, NR = WIDE ? 2 : 1, KT = C::TILE / 16;  // KT: 16-key tiles of scores
+  constexpr int CT = D / 16;                                       // 16-channel tiles of outputs
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int hb = (p.group + C::ROWS - 1) / C::ROWS;
   const int s = blockIdx.x, kvh = blockIdx.y / hb, h0 = (blockIdx.y % hb) * C::ROWS, b = blockIdx.z;
@@ -241,6 +294,10 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     src[x] = (KV4 ? p.cache[x].codes : reinterpret_cast<const uint8_t*>(p.rows[x])) + row0 * C::ROW_BYTES;
 
   const int n_tiles = (n + C::TILE - 1) / C::TILE;
+  // 32 granules further is whole lines further, so a lane's place in every 512 bytes is the same.
+  const uint32_t lane_to = stage0 + cache_granule<D, KV4>(lane);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) src[x] += lane * 16;
   auto fetch = [&](int tile, int stage) {
     if (tile < n_tiles) {
       const int left = n - tile * C::TILE;
@@ -249,10 +306,16 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int i = 0; i < C::HALF_BYTES / 512; ++i) {
-          const int gi = i * 32 + lane;
-          const bool on = gi / (C::ROW_BYTES / 16) < left;  // rows past the length read as zeros
-          cp_async16(stage0 + stage * C::STAGE_BYTES + x * C::HALF_BYTES + cache_granule<D, KV4>(gi),
-                     src[x] + (on ? at + gi * 16 : 0), on);
+          const uint32_t to = lane_to + stage * C::STAGE_BYTES + x * C::HALF_BYTES + (KV4 ? i * 512 : 0);
+          if constexpr (KV4) {
+            // rows past the length are left out: any codes will do where the weights are 0
+            if ((i * 32 + lane) / (C::ROW_BYTES / 16) < left) cp_async16(to, src[x] + at + i * 512);
+          } else {
+            const int gi = i * 32 + lane;
+            const bool on = gi / (C::ROW_BYTES / 16) < left;  // rows past the length read as zeros
+            cp_async16_or_zero(stage0 + stage * C::STAGE_BYTES + x * C::HALF_BYTES + cache_granule<D, KV4>(gi),
+                               src[x] + (on ? at + i * 512 : 0), on);
+          }
         }
     }
     cp_async_commit();
@@ -278,20 +341,35 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 
   CacheQuery<D, KV4, WIDE> q;
   q.load(p.Q + head0 * D, heads, lane);
-  const float c2 = KV4 ? p.scale_log2 * 0x1p12f : p.scale_log2;  // 4-bit: 2^24 2^(e - 14) = 2^12 norm
+  // A thread's columns are the heads 8 x + 2 t + y (y = 0, 1).
+  float c2[NR][2];
+#pragma unroll
+  for (int x = 0; x < NR; ++x)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      // 4-bit: 2^24 2^(e - 14) = 2^12 norm; where |scale q| is beyond 2^117, finite all the same
+      const float norm = __shfl_sync(0xffffffffu, q.norm[x], 8 * t + 4 * y);
+      c2[x][y] = KV4 ? fminf(fmaxf(p.scale_log2 * 0x1p12f * norm, -FLT_MAX), FLT_MAX) : p.scale_log2;
+    }
 
-  float m_ref[NR], l[NR], om[NR][KV4 ? NG : 1], o[CG][4];
+  // Outputs, transposed: rows are channels (4-bit: tile 2 g + h holds channels 32 g + 4 r + 2 h and, in rows 8 .. 15, + 1;
+  // bf16: 16 c + r and + 8), columns heads.  om: sums of p m.
+  float m_ref[NR][2], l[NR][2], om[NR][2][KV4 ? NG : 1], o[CT][NR][4];
 #pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    m_ref[x] = NEG_INF;
-    l[x] = 0.f;
+  for (int x = 0; x < NR; ++x)
 #pragma unroll
-    for (int g = 0; g < (KV4 ? NG : 1); ++g) om[x][g] = 0.f;
-  }
+    for (int y = 0; y < 2; ++y) {
+      m_ref[x][y] = NEG_INF;
+      l[x][y] = 0.f;
 #pragma unroll
-  for (int c = 0; c < CG; ++c)
+      for (int g = 0; g < (KV4 ? NG : 1); ++g) om[x][y][g] = 0.f;
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][x][i] = 0.f;
   int f_exp = 1000;  // 4-bit: p s is multiplied by 2^f_exp (1000: not chosen yet)
   float f = 0.f;
 
@@ -300,61 +378,42 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     cp_async_wait<C::STAGES - 2>();
     if constexpr (KV4) {
       __syncwarp();  // the last tile's scales have been read
-      // The scales as fp32 for the whole warp: [key pair][group][2] for each of K's s, K's m, V's s, V's m.
+      // The scales for the whole warp, [key][group] of K's s, K's raw words (for m), V's s, V's m.
       const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&raw[0]);
       const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&raw[1]);
-      uint32_t top = 0;  // the largest V scale
+      float sv[NG], top = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const uint32_t sb = w1[g] & 0xFFFFu;
-        top = max(top, sb <= 0x7F80u ? sb : 0u);  // NaN scales do not count
+        sv[g] = __uint_as_float(w1[g] << 16);
+        top = fmaxf(top, fabsf(sv[g]));  // NaN scales do not count
       }
-      const bool grow = f_exp == 1000 || bf16_bits_to_float(top) * f >= 0x1p11f;
-      if (__any_sync(0xffffffffu, grow)) {
-        const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 7) - 127;
+      if (__any_sync(0xffffffffu, top * f >= 0x1p11f || f_exp == 1000)) {
+        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23) - 127;
         const int f_new = min(9 - e, 126);
         if (f_exp != 1000) {
-          const float down = exp2_int(f_new - f_exp) * (f_new - f_exp < -126 ? 0.f : 1.f);
+          const float down = f_new - f_exp < -126 ? 0.f : exp2_int(f_new - f_exp);
 #pragma unroll
-          for (int c = 0; c < CG; ++c)
+          for (int c = 0; c < CT; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[c][i] *= down;
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[c][x][i] *= down;
         }
         f_exp = f_new;
         f = exp2_int(f_exp);
       }
-      const bool odd = lane & 1;
-      const uint32_t to = scales0 + (uint32_t)((lane >> 1) * NG * 8 + (odd ? NG * 4 : 0));
+      const uint32_t to = scales0 + (uint32_t)(lane * NG * 4);
+      float k[NG], mv[NG];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t* w = x ? w1 : w0;
-        // even lanes take the first half of the groups of both keys, odd lanes the second
-        uint32_t mine[NG / 2], other[NG / 2];
-#pragma unroll
-        for (int g = 0; g < NG / 2; ++g) {
-          const uint32_t give = odd ? w[g] : w[NG / 2 + g];
-          mine[g] = odd ? w[NG / 2 + g] : w[g];
-          other[g] = __shfl_xor_sync(0xffffffffu, give, 1);
-        }
-        float sv[NG], mv[NG];  // (group, key of the pair)
-#pragma unroll
-        for (int g = 0; g < NG / 2; ++g) {
-          const uint32_t lo = odd ? other[g] : mine[g], hi = odd ? mine[g] : other[g];
-          const float k = x ? f : 1.f;
-          sv[2 * g] = __uint_as_float(lo << 16) * k;
-          sv[2 * g + 1] = __uint_as_float(hi << 16) * k;
-          mv[2 * g] = __uint_as_float(lo & 0xFFFF0000u);
-          mv[2 * g + 1] = __uint_as_float(hi & 0xFFFF0000u);
-        }
-        const uint32_t at = to + x * 2 * (C::TILE * NG * 4);
-        if constexpr (NG == 4) {
-          sts128(at, sv[0], sv[1], sv[2], sv[3]);
-          sts128(at + C::TILE * NG * 4, mv[0], mv[1], mv[2], mv[3]);
-        } else {
-          asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(at), "f"(sv[0]), "f"(sv[1]) : "memory");
-          asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(at + C::TILE * NG * 4), "f"(mv[0]), "f"(mv[1]) : "memory");
-        }
+      for (int g = 0; g < NG; ++g) {
+        k[g] = __uint_as_float(w0[g] << 16);
+        sv[g] *= f;
+        mv[g] = __uint_as_float(w1[g] & 0xFFFF0000u);
       }
+      sts_row<NG>(to, k);
+      sts_row<NG>(to + C::TILE * NG * 4, reinterpret_cast<const float*>(w0));
+      sts_row<NG>(to + 2 * C::TILE * NG * 4, sv);
+      sts_row<NG>(to + 3 * C::TILE * NG * 4, mv);
     }
     __syncwarp();
     fetch(tile + (C::STAGES - 1) * C::WARPS, stage == 0 ? C::STAGES - 1 : stage - 1);
@@ -363,135 +422,162 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     stage = stage == C::STAGES - 1 ? 0 : stage + 1;
 
     // ---------------------------------------------------------------- scores, base 2
-    float sc[NT][2 * NR];
+    float sc[KT][NR][4];  // (key r, heads 2 t, 2 t + 1), (key r + 8, the same heads)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int kt = 0; kt < KT; ++kt) {
       if constexpr (KV4) {
-        const int row = nt * 8 + r;
-        uint32_t w[NG];  // pieces of groups (0, 1), (2, 3) of chunk 2 t, then of chunk 2 t + 1
-        if constexpr (D == 128) {
-          const uint4 v = lds<uint4>(sK + cache_granule<D, KV4>(row * 4 + t));
-          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
-          const uint2 v = lds<uint2>(sK + cache_granule<D, KV4>(row * 2 + (t >> 1)) + (t & 1) * 8);
-          w[0] = v.x, w[1] = v.y;
+        uint32_t w[2][NG];  // keys r, r + 8: pieces of groups (0, 1), (2, 3) of chunk 2 t, then of chunk 2 t + 1
+        float ks[2][NG];
+        uint32_t km[2];     // the minima of group t: the A operand of the product with the group sums
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int row = kt * 16 + y * 8 + r;
+          if constexpr (D == 128) {
+            const uint4 v = lds<uint4>(sK + cache_granule<D, KV4>(row * 4 + t));
+            w[y][0] = v.x, w[y][1] = v.y, w[y][2] = v.z, w[y][3] = v.w;
+          } else {
+            const uint2 v = lds<uint2>(sK + cache_granule<D, KV4>(row * 2 + (t >> 1)) + (t & 1) * 8);
+            w[y][0] = v.x, w[y][1] = v.y;
+          }
+          lds_row<NG>(scales0 + (uint32_t)(row * NG * 4), ks[y]);
+          km[y] = lds<uint32_t>(scales0 + C::TILE * NG * 4 + (uint32_t)((row * NG + (t & (NG - 1))) * 4)) & 0xFFFF0000u;
         }
-        const uint32_t sat = scales0 + (uint32_t)((nt * 4 + t) * NG * 8);
-        float2 sum[NR];
 #pragma unroll
-        for (int x = 0; x < NR; ++x) sum[x] = make_float2(0.f, 0.f);
+        for (int x = 0; x < NR; ++x) mma1688_tf32_first(sc[kt][x], km[0], km[1], km[0], km[1], q.sum[x][0], q.sum[x][1]);
 #pragma unroll
-        for (int g2 = 0; g2 < NG / 2; ++g2) {
-          const uint4 ss = lds<uint4>(sat + g2 * 16), mm = lds<uint4>(sat + C::TILE * NG * 4 + g2 * 16);
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+          const uint32_t u0 = __byte_perm(w[0][g >> 1], w[0][NG / 2 + (g >> 1)], sel), v0 = u0 >> 8;
+          const uint32_t u1 = __byte_perm(w[1][g >> 1], w[1][NG / 2 + (g >> 1)], sel), v1 = u1 >> 8;
+          const uint32_t a0[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+          const uint32_t a1[4] = {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u};
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int g = 2 * g2 + y;
-            const uint32_t u = __byte_perm(w[g2], w[NG / 2 + g2], y ? 0x7632 : 0x5410), u8 = u >> 8;
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<true>(c, q.a[2 * g][0], q.a1(2 * g), q.a[2 * g][1], q.a3(2 * g), u & 0x000F000Fu, u & 0x00F000F0u);
-            mma16816<true>(c, q.a[2 * g + 1][0], q.a1(2 * g + 1), q.a[2 * g + 1][1], q.a3(2 * g + 1), u8 & 0x000F000Fu,
-                           u8 & 0x00F000F0u);
-            const float2 s2 = make_float2(__uint_as_float(y ? ss.z : ss.x), __uint_as_float(y ? ss.w : ss.y));
-            const float2 m2 = make_float2(__uint_as_float(y ? mm.z : mm.x), __uint_as_float(y ? mm.w : mm.y));
+          for (int x = 0; x < NR; ++x) {
+            float c[4];
+            mma16816_first(c, a0[0], a0[1], a0[2], a0[3], q.b[x][2 * g][0], q.b[x][2 * g][1]);
+            mma16816<true>(c, a1[0], a1[1], a1[2], a1[3], q.b[x][2 * g + 1][0], q.b[x][2 * g + 1][1]);
 #pragma unroll
-            for (int x = 0; x < NR; ++x) {
-              sum[x] = sm100::ffma2(s2, make_float2(c[2 * x], c[2 * x + 1]), sum[x]);
-              sum[x] = sm100::ffma2(m2, make_float2(q.sum[x][g], q.sum[x][g]), sum[x]);
-            }
+            for (int i = 0; i < 4; ++i) sc[kt][x][i] = fmaf(ks[i >> 1][g], c[i], sc[kt][x][i]);
           }
         }
-#pragma unroll
-        for (int x = 0; x < NR; ++x) {
-          sc[nt][2 * x] = sum[x].x * c2 * q.norm[x];
-          sc[nt][2 * x + 1] = sum[x].y * c2 * q.norm[x];
-        }
       } else {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        const int row = nt * 8 + (lane & 7);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t bfrag[4];
-          ldmatrix4<false>(bfrag, sK + cache_granule<D, KV4>(row * (D / 8) + 4 * k + (lane >> 3)));
-          mma16816<false>(c, q.a[2 * k][0], q.a1(2 * k), q.a[2 * k][1], q.a3(2 * k), bfrag[0], bfrag[1]);
-          mma16816<false>(c, q.a[2 * k + 1][0], q.a1(2 * k + 1), q.a[2 * k + 1][1], q.a3(2 * k + 1), bfrag[2], bfrag[3]);
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[kt][x][i] = 0.f;
+        const int row = kt * 16 + (lane & 15);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t a[4];
+          ldmatrix4<false>(a, sK + cache_granule<D, KV4>(row * (D / 8) + 2 * k + (lane >> 4)));
+#pragma unroll
+          for (int x = 0; x < NR; ++x) mma16816<false>(sc[kt][x], a[0], a[1], a[2], a[3], q.b[x][k][0], q.b[x][k][1]);
         }
-#pragma unroll
-        for (int i = 0; i < 2 * NR; ++i) sc[nt][i] = c[i] * c2;
       }
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[kt][x][i] *= c2[x][i & 1];
     }
     if (p.scores) {
 #pragma unroll
       for (int x = 0; x < NR; ++x)
-        if (r + 8 * x < heads) {
-          float* to = p.scores + (head0 + r + 8 * x) * p.score_stride + k0 + tile * C::TILE + 2 * t;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (tile * C::TILE + nt * 8 + 2 * t < n)  // the stride leaves room for the pair
-              *reinterpret_cast<float2*>(to + nt * 8) = make_float2(sc[nt][2 * x], sc[nt][2 * x + 1]);
+        for (int i = 0; i < 4; ++i) {
+          const int h = 8 * x + 2 * t + (i & 1);
+          if (h < heads) {
+            float* to = p.scores + (head0 + h) * p.score_stride + k0;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              const int j = tile * C::TILE + kt * 16 + (i >> 1) * 8 + r;
+              if (j < n) to[j] = sc[kt][x][i];
+            }
+          }
         }
     }
     if ((tile + 1) * C::TILE > n) {  // the last tile: keys past the length
       const int left = n - tile * C::TILE;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int i = 0; i < 2 * NR; ++i)
-          if (nt * 8 + 2 * t + (i & 1) >= left) sc[nt][i] = NEG_INF;
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (kt * 16 + (i >> 1) * 8 + r >= left) sc[kt][x][i] = NEG_INF;
     }
 
     // ---------------------------------------------------------------- online softmax
-    float mt[NR];
+    float mt[NR][2];
     bool move = false;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      mt[x] = NEG_INF;
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mt[x] = sm100::max3f(mt[x], sc[nt][2 * x], sc[nt][2 * x + 1]);
-      mt[x] = fmaxf(mt[x], __shfl_xor_sync(0xffffffffu, mt[x], 1));
-      mt[x] = fmaxf(mt[x], __shfl_xor_sync(0xffffffffu, mt[x], 2));
-      move |= mt[x] > m_ref[x] + 4.f;
-    }
+      for (int y = 0; y < 2; ++y) {
+        float m = fmaxf(sc[0][x][y], sc[0][x][2 + y]);
+#pragma unroll
+        for (int kt = 1; kt < KT; ++kt) m = sm100::max3f(m, sc[kt][x][y], sc[kt][x][2 + y]);
+        mt[x][y] = m;
+        move |= m > m_ref[x][y] + 4.f;
+      }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        const float mn = fmaxf(m_ref[x], mt[x]);
-        const float alpha = m_ref[x] == NEG_INF ? 0.f : sm100::ex2_approx(m_ref[x] - mn);
-        m_ref[x] = mn;
-        l[x] *= alpha;
+      for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int g = 0; g < (KV4 ? NG : 1); ++g) om[x][g] *= alpha;
+        for (int y = 0; y < 2; ++y) {
+          float m = fmaxf(m_ref[x][y], mt[x][y]);
 #pragma unroll
-        for (int c = 0; c < CG; ++c) {
-          o[c][2 * x] *= alpha;
-          o[c][2 * x + 1] *= alpha;
-          if (!WIDE && !KV4) {  // rows 8 .. 15 hold the second parts of the same heads
-            o[c][2] *= alpha;
-            o[c][3] *= alpha;
+          for (int off = 4; off <= 16; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+          const float alpha = m_ref[x][y] == NEG_INF ? 0.f : sm100::ex2_approx(m_ref[x][y] - m);
+          m_ref[x][y] = m;
+          l[x][y] *= alpha;
+#pragma unroll
+          for (int g = 0; g < (KV4 ? NG : 1); ++g) om[x][y][g] *= alpha;
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            o[c][x][y] *= alpha;
+            o[c][x][2 + y] *= alpha;
           }
         }
-      }
     }
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const float m = m_ref[x] == NEG_INF ? 0.f : m_ref[x];
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        sc[nt][2 * x] = sm100::ex2_approx(sc[nt][2 * x] - m);
-        sc[nt][2 * x + 1] = sm100::ex2_approx(sc[nt][2 * x + 1] - m);
-        l[x] += sc[nt][2 * x] + sc[nt][2 * x + 1];
+      for (int i = 0; i < 4; ++i) {
+        const float m = m_ref[x][i & 1] == NEG_INF ? 0.f : m_ref[x][i & 1];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+          sc[kt][x][i] = sm100::ex2_approx(sc[kt][x][i] - m);
+          l[x][i & 1] += sc[kt][x][i];
+        }
       }
-    }
 
     // ---------------------------------------------------------------- outputs, 16 keys a step
 #pragma unroll
-    for (int kk = 0; kk < NT / 2; ++kk) {
+    for (int kt = 0; kt < KT; ++kt) {
       if constexpr (KV4) {
+        uint32_t ps[NG][NR][2];  // p s, the B operand: [group][eight heads][eight keys]
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t at = scales0 + 2 * (C::TILE * NG * 4) + (uint32_t)((kt * 16 + y * 8 + r) * NG * 4);
+          float vs[NG], vm[NG];  // of key r + 8 y
+          lds_row<NG>(at, vs);
+          lds_row<NG>(at + C::TILE * NG * 4, vm);
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+              const float p0 = sc[kt][x][2 * y], p1 = sc[kt][x][2 * y + 1];
+              ps[g][x][y] = transpose8x8(pack_f16x2(p0 * vs[g], p1 * vs[g]));
+              om[x][0][g] = fmaf(p0, vm[g], om[x][0][g]);
+              om[x][1][g] = fmaf(p1, vm[g], om[x][1][g]);
+            }
+        }
         uint32_t w[2][2][NG / 2];  // [eight keys][key of the pair][pieces of two groups]
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = kk * 16 + y * 8 + 2 * t + e;
+            const int row = kt * 16 + y * 8 + 2 * t + e;
             if constexpr (D == 128) {
               const uint2 v = lds<uint2>(sV + cache_granule<D, KV4>(row * 4 + (r >> 1)) + (r & 1) * 8);
               w[y][e][0] = v.x, w[y][e][1] = v.y;
@@ -499,36 +585,17 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
               w[y][e][0] = lds<uint32_t>(sV + cache_granule<D, KV4>(row * 2 + (r >> 2)) + (r & 3) * 4);
             }
           }
-        const uint32_t sat = scales0 + 2 * (C::TILE * NG * 4);
 #pragma unroll
-        for (int g2 = 0; g2 < NG / 2; ++g2) {
-          uint4 ss[2], mm[2];
+        for (int g = 0; g < NG; ++g) {
+          const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+          const uint32_t u0 = __byte_perm(w[0][0][g >> 1], w[0][1][g >> 1], sel), v0 = u0 >> 8;
+          const uint32_t u1 = __byte_perm(w[1][0][g >> 1], w[1][1][g >> 1], sel), v1 = u1 >> 8;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t at = sat + (uint32_t)((kk * 8 + y * 4 + t) * NG * 8 + g2 * 16);
-            ss[y] = lds<uint4>(at);
-            mm[y] = lds<uint4>(at + C::TILE * NG * 4);
-          }
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const int g = 2 * g2 + z;
-            uint32_t a[2][2] = {{0u, 0u}, {0u, 0u}};  // [row half][eight keys]
-#pragma unroll
-            for (int x = 0; x < NR; ++x)
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float p0 = sc[2 * kk + y][2 * x], p1 = sc[2 * kk + y][2 * x + 1];
-                a[x][y] = pack_f16x2(p0 * __uint_as_float(z ? ss[y].z : ss[y].x), p1 * __uint_as_float(z ? ss[y].w : ss[y].y));
-                om[x][g] = fmaf(p0, __uint_as_float(z ? mm[y].z : mm[y].x), om[x][g]);
-                om[x][g] = fmaf(p1, __uint_as_float(z ? mm[y].w : mm[y].y), om[x][g]);
-              }
-            const uint32_t u0 = __byte_perm(w[0][0][g2], w[0][1][g2], z ? 0x7632 : 0x5410);
-            const uint32_t u1 = __byte_perm(w[1][0][g2], w[1][1][g2], z ? 0x7632 : 0x5410);
-            const uint32_t v0 = u0 >> 8, v1 = u1 >> 8;
-            mma16816<true>(o[4 * g], a[0][0], a[1][0], a[0][1], a[1][1], u0 & 0x000F000Fu, u1 & 0x000F000Fu);
-            mma16816<true>(o[4 * g + 1], a[0][0], a[1][0], a[0][1], a[1][1], u0 & 0x00F000F0u, u1 & 0x00F000F0u);
-            mma16816<true>(o[4 * g + 2], a[0][0], a[1][0], a[0][1], a[1][1], v0 & 0x000F000Fu, v1 & 0x000F000Fu);
-            mma16816<true>(o[4 * g + 3], a[0][0], a[1][0], a[0][1], a[1][1], v0 & 0x00F000F0u, v1 & 0x00F000F0u);
+          for (int x = 0; x < NR; ++x) {
+            mma16816<true>(o[2 * g][x], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu, u1 & 0x00F000F0u, ps[g][x][0],
+                           ps[g][x][1]);
+            mma16816<true>(o[2 * g + 1][x], v0 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x000F000Fu, v1 & 0x00F000F0u,
+                           ps[g][x][0], ps[g][x][1]);
           }
         }
       } else {
@@ -537,23 +604,21 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         for (int x = 0; x < NR; ++x)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float p0 = sc[2 * kk + y][2 * x], p1 = sc[2 * kk + y][2 * x + 1];
-            hi[x][y] = sm100::pack_bf16x2(p0, p1);
-            lo[x][y] = sm100::pack_bf16x2(p0 - __uint_as_float(hi[x][y] << 16), p1 - __uint_as_float(hi[x][y] & 0xFFFF0000u));
+            const float p0 = sc[kt][x][2 * y], p1 = sc[kt][x][2 * y + 1];
+            const uint32_t h = sm100::pack_bf16x2(p0, p1);
+            hi[x][y] = transpose8x8(h);
+            lo[x][y] =
+                transpose8x8(sm100::pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u)));
           }
 #pragma unroll
-        for (int c = 0; c < CG / 2; ++c) {
+        for (int c = 0; c < CT; ++c) {
           uint32_t v[4];
-          const int row = kk * 16 + (lane & 15);
-          ldmatrix4<true>(v, sV + cache_granule<D, KV4>(row * (D / 8) + 2 * c + (lane >> 4)));
+          const int row = kt * 16 + (lane & 7) + ((lane >> 4) << 3);
+          ldmatrix4<true>(v, sV + cache_granule<D, KV4>(row * (D / 8) + 2 * c + ((lane >> 3) & 1)));
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if constexpr (WIDE) {
-              mma16816<false>(o[2 * c + y], hi[0][0], hi[NR - 1][0], hi[0][1], hi[NR - 1][1], v[2 * y], v[2 * y + 1]);
-              mma16816<false>(o[2 * c + y], lo[0][0], lo[NR - 1][0], lo[0][1], lo[NR - 1][1], v[2 * y], v[2 * y + 1]);
-            } else {
-              mma16816<false>(o[2 * c + y], hi[0][0], lo[0][0], hi[0][1], lo[0][1], v[2 * y], v[2 * y + 1]);
-            }
+          for (int x = 0; x < NR; ++x) {
+            mma16816<false>(o[c][x], v[0], v[1], v[2], v[3], hi[x][0], hi[x][1]);
+            mma16816<false>(o[c][x], v[0], v[1], v[2], v[3], lo[x][0], lo[x][1]);
           }
         }
       }
@@ -563,59 +628,59 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 
   // ------------------------------------------------------------------ the warps of the CTA together
 #pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-    if constexpr (KV4)
+  for (int x = 0; x < NR; ++x)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        om[x][g] += __shfl_xor_sync(0xffffffffu, om[x][g], 1);
-        om[x][g] += __shfl_xor_sync(0xffffffffu, om[x][g], 2);
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int off = 4; off <= 16; off <<= 1) {
+        l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
+        if constexpr (KV4)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) om[x][y][g] += __shfl_xor_sync(0xffffffffu, om[x][y][g], off);
       }
-  }
   __syncthreads();  // every warp is done with its stages
   float* join = reinterpret_cast<float*>(smem);
   constexpr int JOIN = C::JOIN_BYTES / 4;
   {
     float* mine = join + warp * JOIN;
     // 4-bit: back from 2^f_exp and 2^-24, in two exact steps
-    const int back = 24 - f_exp;
+    const int back = f_exp == 1000 ? 0 : 24 - f_exp;
     const float b0 = exp2_int(back / 2), b1 = exp2_int(back - back / 2);
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
-      const int row = r + 8 * x;
-      if (t == 0) {
-        mine[C::ROWS * D + row] = m_ref[x];
-        mine[C::ROWS * D + C::ROWS + row] = l[x];
-      }
-      float* to = mine + row * D;
-#pragma unroll
-      for (int c = 0; c < CG; ++c)
+      if (r == 0) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float v = o[c][2 * x + y];
-          if constexpr (KV4) {
-            const int g = c >> 2, i = c & 3;
-            if (f_exp == 1000) v = 0.f;
-            to[32 * g + 8 * t + 4 * y + i] = fmaf(v * b0 * (i & 1 ? 0.0625f : 1.f), b1, om[x][g]);
-          } else {
-            if (!WIDE) v += o[c][2 + y];
-            to[8 * c + 2 * t + y] = v;
-          }
+          float* stat = mine + C::ROWS * D + (8 * x + 2 * t + y) * C::STATS;
+          stat[0] = m_ref[x][y];
+          stat[1] = l[x][y];
+          if constexpr (KV4)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) stat[2 + g] = om[x][y][g];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 8 * x + 2 * t + (i & 1), up = i >> 1;
+          const int ch = KV4 ? 32 * (c >> 1) + 4 * r + 2 * (c & 1) + up : 16 * c + r + 8 * up;
+          mine[row * D + ch] = KV4 ? o[c][x][i] * (up ? b0 * 0.0625f : b0) * b1 : o[c][x][i];
         }
     }
   }
   __syncthreads();
   for (int idx = threadIdx.x; idx < heads * D; idx += C::THREADS) {
     const int row = idx / D, e = idx % D;
+    const float* stat = join + C::ROWS * D + row * C::STATS;
     float M = NEG_INF, L = 0.f, v = 0.f;
 #pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, join[w * JOIN + C::ROWS * D + row]);
+    for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, stat[w * JOIN]);
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-      const float a = sm100::ex2_approx(join[w * JOIN + C::ROWS * D + row] - M);
-      L = fmaf(a, join[w * JOIN + C::ROWS * D + C::ROWS + row], L);
-      v = fmaf(a, join[w * JOIN + row * D + e], v);
+      const float a = sm100::ex2_approx(stat[w * JOIN] - M);
+      L = fmaf(a, stat[w * JOIN + 1], L);
+      v = fmaf(a, join[w * JOIN + idx] + (KV4 ? stat[w * JOIN + 2 + e / 32] : 0.f), v);
     }
     const size_t part = (head0 + row) * p.n_split + s;
     p.part_o[part * D + e] = v / L;
