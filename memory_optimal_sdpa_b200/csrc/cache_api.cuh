@@ -112,53 +112,67 @@ extern "C" int sdpa_kv4_load(const void* k_codes, const void* k_scales, const vo
 // ------------------------------------------------------------------ decode over a bounded cache
 namespace {
 
-// Keys per split (a multiple of 128): the largest of 2048 .. 128 whose grid over the full cache still has
-// six CTAs per SM.
-int cache_chunk(long long units, long long n_cap) {
-  int chunk = 2048;
-  while (chunk > 128 && units * ((n_cap + chunk - 1) / chunk) < 148LL * 6) chunk >>= 1;
-  return chunk;
-}
-
-// Query heads that one CTA takes: up to 8, or up to 16 where the group has more.
-int cache_head_block(int group) { return group > 8 ? 16 : 8; }
-
-int cache_units(long long batch, int heads_q, int heads_kv) {
-  const int group = heads_q / heads_kv, block = cache_head_block(group);
-  return (int)(batch * heads_kv * ((group + block - 1) / block));
-}
-
-// Floats: one log-sum-exp (base 2) and d outputs per (head, split), and the scores per (head, row).
 long long cache_score_stride(long long n_cap) { return (n_cap + 3) / 4 * 4; }
 
-size_t cache_ws_size(int batch, int heads_q, int heads_kv, int n_cap, int d, bool with_acc) {
+// Query heads per unit of work: up to 8, or up to 16 where the group has more.
+int cache_unit_heads(int group) { return group > 8 ? 16 : 8; }
+
+// CTAs that share the work: what fits on the 148 SMs at once, as workspace sizes have to be known without a GPU.
+template <int D, bool KV4, bool WIDE>
+constexpr int kCacheCtas = 148 * sdpa::CacheCfg<D, KV4, WIDE>::MIN_BLOCKS;
+
+template <int D, bool KV4>
+int cache_ctas_for(bool wide) {
+  return wide ? kCacheCtas<D, KV4, true> : kCacheCtas<D, KV4, false>;
+}
+int cache_ctas(int d, bool kv4, bool wide) {
+  if (d == 64) return kv4 ? cache_ctas_for<64, true>(wide) : cache_ctas_for<64, false>(wide);
+  return kv4 ? cache_ctas_for<128, true>(wide) : cache_ctas_for<128, false>(wide);
+}
+
+// Partial results of the segments (at most one per unit and one more per CTA).
+struct CacheParts {
+  long long heads, rows;  // query heads per unit; rows of all segments
+};
+CacheParts cache_parts(long long batch, int heads_q, int heads_kv, int d, bool kv4) {
+  const int group = heads_q / heads_kv, rows = cache_unit_heads(group);
+  const long long units = batch * heads_kv * ((group + rows - 1) / rows);
+  return {rows, (units + cache_ctas(d, kv4, rows == 16)) * rows};
+}
+
+// Floats: d outputs and one log-sum-exp per row of the partial results (a multiple of 8 rows), and the scores per (head,
+// cache row); then one 64-bit number per sequence and one more.
+size_t cache_ws_size(int batch, int heads_q, int heads_kv, int n_cap, int d, bool kv4, bool with_acc) {
   if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || n_cap <= 0 || !cache_head_dim(d)) return 0;
-  const long long chunk = cache_chunk(cache_units(batch, heads_q, heads_kv), n_cap);
-  const long long ns = (n_cap + chunk - 1) / chunk;
-  const long long lse = ((long long)batch * heads_q * ns + 3) / 4 * 4;
-  return (size_t)((long long)batch * heads_q * (ns * d + (with_acc ? cache_score_stride(n_cap) : 0)) + lse) * sizeof(float);
+  const CacheParts parts = cache_parts(batch, heads_q, heads_kv, d, kv4);
+  const long long scores = with_acc ? (long long)batch * heads_q * cache_score_stride(n_cap) : 0;
+  return (size_t)(parts.rows * (d + 1) + scores) * sizeof(float) + (size_t)(batch + 2) / 2 * 2 * sizeof(long long);
 }
 
 template <int D, bool KV4, bool WIDE>
-int launch_cache_split(const sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
+int launch_cache_split(const sdpa::CacheDecodeParams& p, cudaStream_t s) {
   using Cfg = sdpa::CacheCfg<D, KV4, WIDE>;
   auto kern = sdpa::sdpa_cache_split_kernel<D, KV4, WIDE>;
   static std::atomic<uint64_t> ready{0};
   if (int e = allow_smem(kern, Cfg::SMEM_BYTES, ready)) return e;
-  const int hb = (p.group + Cfg::ROWS - 1) / Cfg::ROWS;
-  kern<<<dim3((unsigned)p.n_split, (unsigned)(p.H_kv * hb), (unsigned)batch), Cfg::THREADS, Cfg::SMEM_BYTES, s>>>(p);
+  kern<<<(unsigned)p.n_cta, Cfg::THREADS, Cfg::SMEM_BYTES, s>>>(p);
   return launched("cache decode launch");
 }
 
 template <int D, bool KV4>
-int launch_cache_decode(const sdpa::CacheDecodeParams& p, int batch, cudaStream_t s) {
-  const int rc = cache_head_block(p.group) == 16 ? launch_cache_split<D, KV4, true>(p, batch, s)
-                                                  : launch_cache_split<D, KV4, false>(p, batch, s);
+int launch_cache_decode(sdpa::CacheDecodeParams p, cudaStream_t s) {
+  const bool wide = p.rows == 16;
+  p.block = wide ? sdpa::CacheCfg<D, KV4, true>::BLOCK : sdpa::CacheCfg<D, KV4, false>::BLOCK;
+  p.n_cta = cache_ctas_for<D, KV4>(wide);
+  // no more CTAs than blocks of work in a full cache
+  const long long most = (long long)p.B * p.H_kv * p.head_blocks * ((p.n_cap + p.block - 1) / p.block);
+  if (most < p.n_cta) p.n_cta = (int)most;
+  const int rc = wide ? launch_cache_split<D, KV4, true>(p, s) : launch_cache_split<D, KV4, false>(p, s);
   if (rc != SDPA_OK) return rc;
   // a programmatic dependent: its launch overlaps the splits' last wave, and it waits for them itself
   cudaLaunchConfig_t cfg = {};
   const int key_blocks = p.scores ? (p.n_cap + sdpa::CACHE_FINISH_KEYS - 1) / sdpa::CACHE_FINISH_KEYS : 0;
-  cfg.gridDim = dim3((unsigned)(p.group + key_blocks), (unsigned)p.H_kv, (unsigned)batch);
+  cfg.gridDim = dim3((unsigned)(p.head_blocks + key_blocks), (unsigned)p.H_kv, (unsigned)p.B);
   cfg.blockDim = dim3(sdpa::CACHE_FINISH_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -177,7 +191,7 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   if (!aligned16(Q) || !aligned16(O) || !aligned4(kv_lens) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out))
     return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads_q, 1) || !cache_sizes_fit(batch, heads_kv, n_cap)) return SDPA_ERR_UNSUPPORTED;
-  const size_t need = cache_ws_size(batch, heads_q, heads_kv, n_cap, d, acc_out != nullptr);
+  const size_t need = cache_ws_size(batch, heads_q, heads_kv, n_cap, d, kv4, acc_out != nullptr);
   if (!workspace || workspace_bytes < need) return SDPA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SDPA_ERR_MISALIGNED;
   if (int e = check_device()) return e;
@@ -191,27 +205,29 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   p.H_kv = heads_kv;
   p.group = heads_q / heads_kv;
   p.n_cap = n_cap;
-  p.chunk = cache_chunk(cache_units(batch, heads_q, heads_kv), n_cap);
+  const CacheParts parts = cache_parts(batch, heads_q, heads_kv, d, kv4);
+  p.B = batch;
+  p.rows = (int)parts.heads;
+  p.head_blocks = (p.group + p.rows - 1) / p.rows;
   p.score_stride = (int)cache_score_stride(n_cap);
-  p.n_split = (n_cap + p.chunk - 1) / p.chunk;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const size_t bh = (size_t)batch * heads_q;
   p.part_o = (float*)workspace;
-  p.scores = acc_out ? p.part_o + bh * p.n_split * d : nullptr;  // 16-byte rows: the stride is a multiple of 4
-  p.part_lse = p.part_o + bh * (p.n_split * (size_t)d + (acc_out ? (size_t)p.score_stride : 0));
+  p.scores = acc_out ? p.part_o + (size_t)parts.rows * d : nullptr;  // 16-byte rows: the stride is a multiple of 4
+  p.part_lse = p.part_o + (size_t)parts.rows * d + (acc_out ? (size_t)batch * heads_q * p.score_stride : 0);
+  p.seq_at = (long long*)(p.part_lse + parts.rows);
   cudaStream_t s = (cudaStream_t)stream;
-  if (d == 64) return kv4 ? launch_cache_decode<64, true>(p, batch, s) : launch_cache_decode<64, false>(p, batch, s);
-  return kv4 ? launch_cache_decode<128, true>(p, batch, s) : launch_cache_decode<128, false>(p, batch, s);
+  if (d == 64) return kv4 ? launch_cache_decode<64, true>(p, s) : launch_cache_decode<64, false>(p, s);
+  return kv4 ? launch_cache_decode<128, true>(p, s) : launch_cache_decode<128, false>(p, s);
 }
 
 }  // namespace
 
 extern "C" size_t sdpa_decode_kv4_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d, int with_acc) {
-  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc != 0);
+  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, true, with_acc != 0);
 }
 
 extern "C" size_t sdpa_decode_acc_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d) {
-  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, true);
+  return cache_ws_size(batch, heads_q, heads_kv, n_kv_cap, d, false, true);
 }
 
 extern "C" int sdpa_decode_kv4(const void* Q, const void* k_codes, const void* k_scales, const void* v_codes,
@@ -242,8 +258,8 @@ extern "C" int sdpa_decode_acc(const void* Q, const void* K, const void* V, cons
   if (!Q || !K || !V || !kv_lens || !O || !acc_out) return SDPA_ERR_INVALID_ARG;
   if (!aligned16(K) || !aligned16(V)) return SDPA_ERR_MISALIGNED;
   sdpa::CacheDecodeParams p = {};
-  p.rows[0] = (const __nv_bfloat16*)K;
-  p.rows[1] = (const __nv_bfloat16*)V;
+  p.kv[0] = (const __nv_bfloat16*)K;
+  p.kv[1] = (const __nv_bfloat16*)V;
   return cache_decode(p, false, Q, kv_lens, O, LSE, acc, acc_out, batch, heads_q, heads_kv, n_kv_cap, d, scale,
                       workspace, workspace_bytes, stream);
 }

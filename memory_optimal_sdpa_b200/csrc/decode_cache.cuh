@@ -1,11 +1,13 @@
 // decode_cache.cuh -- one query row per head against a bounded cache: bf16 or 4-bit rows, with the
 // attention weights of every key added to an accumulator where asked for.
 //
-// CTA (split s, key/value head and block of its query heads, b) reduces keys [s chunk, s chunk + chunk) of
-// the valid prefix to a normalised partial output and a log-sum-exp (base 2) per query head.  With weights
-// it also writes the scores (base 2, fp32): a key's weight needs the log-sum-exp over all splits, and 4
-// bytes a score, written and read once, cost far less than reading the keys again.
-// sdpa_cache_finish_kernel joins the splits and adds sum_h 2^(score_h - LSE_h) per key.
+// The keys of all (sequence, key/value head, block of query heads) units, in blocks of 64 or 128, are one long
+// line of work that is cut evenly among as many CTAs as fit on the GPU at once: lengths differ, and a
+// wave that is not full costs as much as a full one.  A CTA's cut is one or more segments, each of one unit; a segment gives
+// a normalised partial output and a log-sum-exp (base 2) per query head.  Segment number unit + CTA is unique,
+// as both only grow along the line.  With weights the scores (base 2, fp32) are written too: a key's weight
+// needs the log-sum-exp over all of its unit's segments, and 4 bytes a score, written and read once, cost far less than
+// reading the keys again.  sdpa_cache_finish_kernel joins the segments and adds sum_h 2^(score_h - LSE_h) per key.
 //
 // What bounds it: HBM, if the arithmetic fits under it.  A 4-bit row pair of d = 128 is 160 bytes, 6.9 clocks of an
 // SM's share of HBM, in which 256 codes have to become operands.  So the codes never leave registers:
@@ -41,17 +43,22 @@ namespace sdpa {
 
 struct CacheDecodeParams {
   const __nv_bfloat16* Q;       // [B, Hq, D]
-  const __nv_bfloat16* rows[2]; // bf16 cache K, V
+  const __nv_bfloat16* kv[2];   // bf16 cache K, V
   Kv4Cache cache[2];            // or 4-bit cache K, V
   const int* kv_lens;
-  float* part_o;    // [B, Hq, S, D]
-  float* part_lse;  // [B, Hq, S], base 2
+  float* part_o;    // [units + CTAs, ROWS, D]
+  float* part_lse;  // [units + CTAs, ROWS], base 2
+  long long* seq_at;  // [B + 1]: blocks of work before each sequence, and all of them
   float* scores;    // [B, Hq, score_stride], base 2, or null
   const float* acc;
   float* acc_out;   // [B, Hkv, n_cap]
   __nv_bfloat16* O;
   float* LSE;
-  int H_q, H_kv, group, n_cap, chunk, n_split;
+  int B, H_q, H_kv, group, n_cap;
+  int head_blocks;   // units per (sequence, key/value head)
+  int rows;          // query heads per unit
+  int block;         // keys per block of work
+  int n_cta;
   int score_stride;  // n_cap rounded up to 4
   float scale_log2;
 };
@@ -66,21 +73,91 @@ struct CacheCfg {
   static constexpr int STAGES = 3;
   static constexpr int ROW_BYTES = KV4 ? D / 2 : 2 * D;
   static constexpr int HALF_BYTES = TILE * ROW_BYTES;  // K or V of a tile
-  static constexpr int STAGE_BYTES = 2 * HALF_BYTES;
   static constexpr int NG = D / 32;
-  static constexpr int SCALE_BYTES = KV4 ? 4 * TILE * NG * 4 : 0;  // s and m of K and V, as fp32
+  static constexpr int RAW_BYTES = KV4 ? TILE * NG * 4 : 0;  // the scales of a tile as they are stored, K's or V's
+  static constexpr int STAGE_BYTES = 2 * (HALF_BYTES + RAW_BYTES);
+  static constexpr int SCALE_BYTES = KV4 ? 3 * TILE * NG * 4 : 0;  // K's s, V's s and m as fp32
   static constexpr int WARP_BYTES = STAGES * STAGE_BYTES + SCALE_BYTES;
-  static constexpr int STATS = KV4 ? 2 + NG : 2;                    // m, l and the sums with the minima
-  static constexpr int JOIN_BYTES = ROWS * (D + STATS) * 4;         // a warp's results (over the stages)
+  static constexpr int JOIN_ROW = D + 4;                   // floats: the four columns of a quad meet other banks
+  static constexpr int JOIN_BYTES = ROWS * JOIN_ROW * 4;   // a warp's outputs (over the stages)
   static constexpr int SMEM_BYTES = WARPS * (WARP_BYTES > JOIN_BYTES ? WARP_BYTES : JOIN_BYTES);
-  static constexpr int MIN_BLOCKS = WIDE ? 2 : (KV4 ? 3 : 2);
+  static constexpr int MIN_BLOCKS = WIDE ? 2 : (KV4 ? 3 : 2);  // CTAs per SM
+  static constexpr int BLOCK = WARPS * TILE;                    // keys per block of work
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// The line of work: unit u = b upb + (key/value head, head block), of blocks(b) blocks each.  CTA c takes blocks
+// [c T / n, (c + 1) T / n) of the T there are, with n = min(CTAs, T), so that none of the n is empty.
+struct CacheLine {
+  long long total;  // T
+  int n;
+  __device__ __forceinline__ static int blocks(const CacheDecodeParams& p, int b) {
+    return (cache_len(p.kv_lens, b, p.n_cap) + p.block - 1) / p.block;
+  }
+  // By a whole warp.
+  __device__ __forceinline__ CacheLine(const CacheDecodeParams& p, long long total_) : total(total_) {
+    n = (int)min((long long)p.n_cta, total);
+  }
+  __device__ __forceinline__ CacheLine(const CacheDecodeParams& p, int lane) {
+    int sum = 0;  // below 2^31: batch * heads * n_cap is
+    for (int b = lane; b < p.B; b += 32) sum += blocks(p, b);
+    total = (long long)__reduce_add_sync(0xffffffffu, sum) * p.H_kv * p.head_blocks;
+    n = (int)min((long long)p.n_cta, total);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return c * total / n; }
+  // The CTA that has block x.
+  __device__ __forceinline__ int cta_of(long long x) const { return (int)(((x + 1) * n + total - 1) / total) - 1; }
+  // Runs over the sequences, 32 at a time, with a warp: f(b, blocks before b, blocks of b and before) -> stop.
+  template <class F>
+  __device__ __forceinline__ static void scan(const CacheDecodeParams& p, int lane, F f) {
+    const long long upb = (long long)p.H_kv * p.head_blocks;
+    long long run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane, mine = b < p.B ? blocks(p, b) : 0;
+      int sum = mine;  // inclusive over the lanes
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      if (f(b, run + (sum - mine) * upb, run + sum * upb)) return;
+      run += __shfl_sync(0xffffffffu, sum, 31) * upb;
+    }
+  }
+  // The first sequence whose blocks end past x, and where they begin.
+  __device__ __forceinline__ static long long find(const CacheDecodeParams& p, int lane, long long x, int& found) {
+    long long at = 0;
+    scan(p, lane, [&](int b, long long begin, long long end) {
+      const uint32_t past = __ballot_sync(0xffffffffu, end > x);
+      if (past == 0) return false;
+      const int k = __ffs(past) - 1;
+      found = __shfl_sync(0xffffffffu, b, k);
+      at = __shfl_sync(0xffffffffu, begin, k);
+      return true;
+    });
+    return at;
+  }
+  __device__ __forceinline__ static void write(const CacheDecodeParams& p, int lane) {
+    scan(p, lane, [&](int b, long long begin, long long end) {
+      if (b < p.B) p.seq_at[b] = begin;
+      if (b == p.B - 1) p.seq_at[p.B] = end;
+      return false;
+    });
+  }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void sts_zero(uint32_t dst) {
+  if constexpr (BYTES == 16)
+    asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
+  else
+    asm volatile("st.shared.v2.u32 [%0], {%1,%1};" ::"r"(dst), "r"(0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -195,7 +272,8 @@ struct CacheQuery {
   uint32_t sum[NR][2];
   float norm[NR];  // what this head's scores are multiplied by at the end (a power of two)
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* q, int heads, int lane) {
+  // flip: the sign bits of a negative scale (two bf16 at a time).
+  __device__ __forceinline__ void load(const __nv_bfloat16* q, int heads, uint32_t flip, int lane) {
     const int r = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
@@ -205,7 +283,8 @@ struct CacheQuery {
         float f[NG][8], big = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const uint4 raw = on ? *reinterpret_cast<const uint4*>(row + 32 * g + 8 * t) : make_uint4(0, 0, 0, 0);
+          uint4 raw = on ? *reinterpret_cast<const uint4*>(row + 32 * g + 8 * t) : make_uint4(0, 0, 0, 0);
+          raw.x ^= flip, raw.y ^= flip, raw.z ^= flip, raw.w ^= flip;
           bf16x8_to_f32(raw, f[g]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(f[g][i]));
@@ -244,8 +323,8 @@ struct CacheQuery {
         norm[x] = 1.f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          b[x][k][0] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t) : 0u;
-          b[x][k][1] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8 + 2 * t) : 0u;
+          b[x][k][0] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t) ^ flip : 0u;
+          b[x][k][1] = on ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 8 + 2 * t) ^ flip : 0u;
         }
       }
     }
@@ -273,83 +352,100 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   constexpr int NG = C::NG, NR = WIDE ? 2 : 1, KT = C::TILE / 16;  // KT: 16-key tiles of scores
   constexpr int CT = D / 16;                                       // 16-channel tiles of outputs
   const float NEG_INF = -__int_as_float(0x7f800000);
-  const int hb = (p.group + C::ROWS - 1) / C::ROWS;
-  const int s = blockIdx.x, kvh = blockIdx.y / hb, h0 = (blockIdx.y % hb) * C::ROWS, b = blockIdx.z;
-  const int heads = min(C::ROWS, p.group - h0);
-  const int len = cache_len(p.kv_lens, b, p.n_cap);
-  const int k0 = s * p.chunk;
-  if (k0 >= len) return;
-  const int n = min(p.chunk, len - k0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-  const size_t row0 = ((size_t)b * p.H_kv + kvh) * p.n_cap + k0;
-  const size_t head0 = (size_t)b * p.H_q + (size_t)kvh * p.group + h0;
-
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t stage0 = sm100::smem_u32(smem) + warp * C::WARP_BYTES;
   const uint32_t scales0 = stage0 + C::STAGES * C::STAGE_BYTES;
 
-  const uint8_t* src[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    src[x] = (KV4 ? p.cache[x].codes : reinterpret_cast<const uint8_t*>(p.rows[x])) + row0 * C::ROW_BYTES;
+  const CacheLine line(p, lane);
+  const int cta = blockIdx.x, upb = p.H_kv * p.head_blocks;
+  if (cta >= line.n) return;
+  long long at = line.begin(cta);
+  const long long end = line.begin(cta + 1);
+  __shared__ float2 s_stat[C::WARPS][C::ROWS];  // m, l
+  if (cta == 0 && warp == 0) CacheLine::write(p, lane);
+  int b = 0;
+  long long seq_at = CacheLine::find(p, lane, at, b);  // where sequence b begins
+  int seq_blocks = CacheLine::blocks(p, b);
+
+  for (bool first = true; at < end; first = false) {
+  if (!first) __syncthreads();  // the last segment's results have been read
+  while (at >= seq_at + (long long)upb * seq_blocks) {
+    seq_at += (long long)upb * seq_blocks;
+    seq_blocks = CacheLine::blocks(p, ++b);
+  }
+  const int unit = (int)((at - seq_at) / seq_blocks), block0 = (int)((at - seq_at) % seq_blocks);
+  const int n_blocks = (int)min((long long)(seq_blocks - block0), end - at);
+  at += n_blocks;
+  const size_t part0 = ((size_t)b * upb + unit + cta) * C::ROWS;
+  const int kvh = unit / p.head_blocks, h0 = (unit % p.head_blocks) * C::ROWS;
+  const int heads = min(C::ROWS, p.group - h0);
+  const int k0 = block0 * C::BLOCK;
+  const int n = min(n_blocks * C::BLOCK, cache_len(p.kv_lens, b, p.n_cap) - k0);
+  const size_t row0 = ((size_t)b * p.H_kv + kvh) * p.n_cap + k0;
+  const size_t head0 = (size_t)b * p.H_q + (size_t)kvh * p.group + h0;
 
   const int n_tiles = (n + C::TILE - 1) / C::TILE;
-  // 32 granules further is whole lines further, so a lane's place in every 512 bytes is the same.
-  const uint32_t lane_to = stage0 + cache_granule<D, KV4>(lane);
+  // This lane's places in the next tile to fetch.  32 granules further is whole lines further, so a lane's place in
+  // every 512 bytes of 4-bit rows is the same.
+  const uint8_t* src[2];
+  const uint32_t* src_scales[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) src[x] += lane * 16;
-  auto fetch = [&](int tile, int stage) {
-    if (tile < n_tiles) {
-      const int left = n - tile * C::TILE;
-      const size_t at = (size_t)tile * C::HALF_BYTES;
+  for (int x = 0; x < 2; ++x) {
+    src[x] = (KV4 ? p.cache[x].codes : reinterpret_cast<const uint8_t*>(p.kv[x])) +
+             (row0 + warp * C::TILE) * C::ROW_BYTES + lane * 16;
+    if (KV4) src_scales[x] = p.cache[x].scales + (row0 + warp * C::TILE + lane) * NG;
+  }
+  int left = n - warp * C::TILE;  // keys from there on
+  const uint32_t lane_to = stage0 + cache_granule<D, KV4>(lane), lane_raw = stage0 + 2 * C::HALF_BYTES + lane * (NG * 4);
+  auto fetch = [&](uint32_t put) {  // put: the stage, in bytes
+    if (left > 0) {
+      const bool full = left >= C::TILE;
+      if constexpr (KV4) {  // scales: a lane per key; zeros past the length
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t to = lane_raw + put + x * C::RAW_BYTES;
+          if (full || lane < left)
+            cp_async<NG * 4>(to, src_scales[x]);
+          else
+            sts_zero<NG * 4>(to);
+        }
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int i = 0; i < C::HALF_BYTES / 512; ++i) {
-          const uint32_t to = lane_to + stage * C::STAGE_BYTES + x * C::HALF_BYTES + (KV4 ? i * 512 : 0);
-          if constexpr (KV4) {
-            // rows past the length are left out: any codes will do where the weights are 0
-            if ((i * 32 + lane) / (C::ROW_BYTES / 16) < left) cp_async16(to, src[x] + at + i * 512);
-          } else {
-            const int gi = i * 32 + lane;
-            const bool on = gi / (C::ROW_BYTES / 16) < left;  // rows past the length read as zeros
-            cp_async16_or_zero(stage0 + stage * C::STAGE_BYTES + x * C::HALF_BYTES + cache_granule<D, KV4>(gi),
-                               src[x] + (on ? at + i * 512 : 0), on);
-          }
+          const uint32_t to = (KV4 ? lane_to + i * 512 : stage0 + cache_granule<D, KV4>(i * 32 + lane)) + put + x * C::HALF_BYTES;
+          // rows past the length: bf16 ones become zeros; of 4 bits any codes will do, as their scales are 0
+          if (full || (i * 32 + lane) / (C::ROW_BYTES / 16) < left)
+            cp_async<16>(to, src[x] + i * 512);
+          else if (!KV4)
+            sts_zero<16>(to);
         }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        src[x] += C::WARPS * C::HALF_BYTES;
+        if (KV4) src_scales[x] += C::WARPS * C::TILE * NG;
+      }
+      left -= C::WARPS * C::TILE;
     }
     cp_async_commit();
   };
-  // 4-bit: a lane holds the scales of one key of the coming tile, K's then V's.
-  using Raw = typename std::conditional<D == 128, uint4, uint2>::type;
-  Raw raw[2];
-  auto fetch_scales = [&](int tile) {
-    if constexpr (KV4) {
-      const int j = tile * C::TILE + lane;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Raw v = {};
-        if (j < n) v = __ldg(reinterpret_cast<const Raw*>(p.cache[x].scales + (row0 + j) * NG));
-        raw[x] = v;
-      }
-    }
-  };
-
-#pragma unroll
-  for (int i = 0; i < C::STAGES - 1; ++i) fetch(warp + i * C::WARPS, i);
-  fetch_scales(warp);
+  for (int i = 0; i < C::STAGES - 1; ++i) fetch(i * C::STAGE_BYTES);
 
   CacheQuery<D, KV4, WIDE> q;
-  q.load(p.Q + head0 * D, heads, lane);
+  q.load(p.Q + head0 * D, heads, p.scale_log2 < 0.f ? 0x80008000u : 0u, lane);
   // A thread's columns are the heads 8 x + 2 t + y (y = 0, 1).
   float c2[NR][2];
 #pragma unroll
   for (int x = 0; x < NR; ++x)
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      // 4-bit: 2^24 2^(e - 14) = 2^12 norm; where |scale q| is beyond 2^117, finite all the same
-      const float norm = __shfl_sync(0xffffffffu, q.norm[x], 8 * t + 4 * y);
-      c2[x][y] = KV4 ? fminf(fmaxf(p.scale_log2 * 0x1p12f * norm, -FLT_MAX), FLT_MAX) : p.scale_log2;
+      // 4-bit: 2^24 2^(e - 14) = 2^12 norm.  Finite where |scale q| is beyond 2^117; and not 0 (scale 0), which
+      // would make NaN of the -inf of a key past the length: 2^-126 leaves every other weight 1.
+      const float norm = __shfl_sync(0xffffffffu, q.norm[x], 8 * t + 4 * y), c = fabsf(p.scale_log2);
+      c2[x][y] = fmaxf(KV4 ? fminf(c * 0x1p12f * norm, FLT_MAX) : c, FLT_MIN);
     }
 
   // Outputs, transposed: rows are channels (4-bit: tile 2 g + h holds channels 32 g + 4 r + 2 h and, in rows 8 .. 15, + 1;
@@ -373,14 +469,18 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   int f_exp = 1000;  // 4-bit: p s is multiplied by 2^f_exp (1000: not chosen yet)
   float f = 0.f;
 
-  int stage = 0;
+  uint32_t get = 0;  // this tile's stage, in bytes
   for (int tile = warp; tile < n_tiles; tile += C::WARPS) {
     cp_async_wait<C::STAGES - 2>();
     if constexpr (KV4) {
       __syncwarp();  // the last tile's scales have been read
-      // The scales for the whole warp, [key][group] of K's s, K's raw words (for m), V's s, V's m.
-      const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&raw[0]);
-      const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&raw[1]);
+      // The scales for the whole warp, [key][group] of K's s, V's s, V's m; K's m are taken from where they are.
+      float w0f[NG], w1f[NG];  // this lane's key, as it copied it itself
+      lds_row<NG>(lane_raw + get, w0f);
+      lds_row<NG>(lane_raw + get + C::RAW_BYTES, w1f);
+      uint32_t w0[NG], w1[NG];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) w0[g] = __float_as_uint(w0f[g]), w1[g] = __float_as_uint(w1f[g]);
       float sv[NG], top = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -411,17 +511,15 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         mv[g] = __uint_as_float(w1[g] & 0xFFFF0000u);
       }
       sts_row<NG>(to, k);
-      sts_row<NG>(to + C::TILE * NG * 4, reinterpret_cast<const float*>(w0));
-      sts_row<NG>(to + 2 * C::TILE * NG * 4, sv);
-      sts_row<NG>(to + 3 * C::TILE * NG * 4, mv);
+      sts_row<NG>(to + C::TILE * NG * 4, sv);
+      sts_row<NG>(to + 2 * C::TILE * NG * 4, mv);
     }
     __syncwarp();
-    fetch(tile + (C::STAGES - 1) * C::WARPS, stage == 0 ? C::STAGES - 1 : stage - 1);
-    if (tile + C::WARPS < n_tiles) fetch_scales(tile + C::WARPS);
-    const uint32_t sK = stage0 + stage * C::STAGE_BYTES, sV = sK + C::HALF_BYTES;
-    stage = stage == C::STAGES - 1 ? 0 : stage + 1;
+    fetch(get == 0 ? (C::STAGES - 1) * C::STAGE_BYTES : get - C::STAGE_BYTES);
+    const uint32_t sK = stage0 + get, sV = sK + C::HALF_BYTES;
+    get = get == (C::STAGES - 1) * C::STAGE_BYTES ? 0 : get + C::STAGE_BYTES;
 
-    // ---------------------------------------------------------------- scores, base 2
+    // ---------------------------------------------------------------- scores, to be multiplied by c2
     float sc[KT][NR][4];  // (key r, heads 2 t, 2 t + 1), (key r + 8, the same heads)
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
@@ -440,7 +538,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
             w[y][0] = v.x, w[y][1] = v.y;
           }
           lds_row<NG>(scales0 + (uint32_t)(row * NG * 4), ks[y]);
-          km[y] = lds<uint32_t>(scales0 + C::TILE * NG * 4 + (uint32_t)((row * NG + (t & (NG - 1))) * 4)) & 0xFFFF0000u;
+          km[y] = lds<uint32_t>(sK + 2 * C::HALF_BYTES + (uint32_t)((row * NG + (t & (NG - 1))) * 4)) & 0xFFFF0000u;
         }
 #pragma unroll
         for (int x = 0; x < NR; ++x) mma1688_tf32_first(sc[kt][x], km[0], km[1], km[0], km[1], q.sum[x][0], q.sum[x][1]);
@@ -474,10 +572,6 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
           for (int x = 0; x < NR; ++x) mma16816<false>(sc[kt][x], a[0], a[1], a[2], a[3], q.b[x][k][0], q.b[x][k][1]);
         }
       }
-#pragma unroll
-      for (int x = 0; x < NR; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[kt][x][i] *= c2[x][i & 1];
     }
     if (p.scores) {
 #pragma unroll
@@ -490,7 +584,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
               const int j = tile * C::TILE + kt * 16 + (i >> 1) * 8 + r;
-              if (j < n) to[j] = sc[kt][x][i];
+              if (j < n) to[j] = sc[kt][x][i] * c2[x][i & 1];
             }
           }
         }
@@ -516,8 +610,8 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         float m = fmaxf(sc[0][x][y], sc[0][x][2 + y]);
 #pragma unroll
         for (int kt = 1; kt < KT; ++kt) m = sm100::max3f(m, sc[kt][x][y], sc[kt][x][2 + y]);
-        mt[x][y] = m;
-        move |= m > m_ref[x][y] + 4.f;
+        mt[x][y] = m * c2[x][y];
+        move |= mt[x][y] > m_ref[x][y] + 4.f;
       }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -546,7 +640,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         const float m = m_ref[x][i & 1] == NEG_INF ? 0.f : m_ref[x][i & 1];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-          sc[kt][x][i] = sm100::ex2_approx(sc[kt][x][i] - m);
+          sc[kt][x][i] = sm100::ex2_approx(fmaf(sc[kt][x][i], c2[x][i & 1], -m));
           l[x][i & 1] += sc[kt][x][i];
         }
       }
@@ -558,7 +652,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         uint32_t ps[NG][NR][2];  // p s, the B operand: [group][eight heads][eight keys]
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint32_t at = scales0 + 2 * (C::TILE * NG * 4) + (uint32_t)((kt * 16 + y * 8 + r) * NG * 4);
+          const uint32_t at = scales0 + C::TILE * NG * 4 + (uint32_t)((kt * 16 + y * 8 + r) * NG * 4);
           float vs[NG], vm[NG];  // of key r + 8 y
           lds_row<NG>(at, vs);
           lds_row<NG>(at + C::TILE * NG * 4, vm);
@@ -630,7 +724,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 #pragma unroll
   for (int x = 0; x < NR; ++x)
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int y = 0; y < 2; ++y) {
 #pragma unroll
       for (int off = 4; off <= 16; off <<= 1) {
         l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
@@ -638,136 +732,175 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 #pragma unroll
           for (int g = 0; g < NG; ++g) om[x][y][g] += __shfl_xor_sync(0xffffffffu, om[x][y][g], off);
       }
-  __syncthreads();  // every warp is done with its stages
+      if (r == 0) s_stat[warp][8 * x + 2 * t + y] = make_float2(m_ref[x][y], l[x][y]);
+    }
+  __syncthreads();  // and every warp is done with its stages
   float* join = reinterpret_cast<float*>(smem);
   constexpr int JOIN = C::JOIN_BYTES / 4;
+  const bool whole = n_blocks == seq_blocks;  // the unit has no other segment
   {
-    float* mine = join + warp * JOIN;
     // 4-bit: back from 2^f_exp and 2^-24, in two exact steps
     const int back = f_exp == 1000 ? 0 : 24 - f_exp;
     const float b0 = exp2_int(back / 2), b1 = exp2_int(back - back / 2);
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      if (r == 0) {
+    for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float* stat = mine + C::ROWS * D + (8 * x + 2 * t + y) * C::STATS;
-          stat[0] = m_ref[x][y];
-          stat[1] = l[x][y];
-          if constexpr (KV4)
+      for (int y = 0; y < 2; ++y) {
+        const int row = 8 * x + 2 * t + y;
+        float M = NEG_INF, L = 0.f;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) stat[2 + g] = om[x][y][g];
+        for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, s_stat[w][row].x);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) L = fmaf(sm100::ex2_approx(s_stat[w][row].x - M), s_stat[w][row].y, L);
+        const float mul = sm100::ex2_approx(m_ref[x][y] - M) / L;  // of this warp's sums
+        if (warp == 0 && r == 0 && row < heads) {
+          const float l2 = M + log2f(L);
+          p.part_lse[part0 + row] = l2;
+          if (whole && p.LSE) p.LSE[head0 + row] = l2 * 0.69314718055994531f;
+        }
+        float* to = join + warp * JOIN + row * C::JOIN_ROW;
+        if constexpr (KV4) {
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            float v[4] = {o[2 * g][x][y], o[2 * g][x][2 + y] * 0.0625f, o[2 * g + 1][x][y], o[2 * g + 1][x][2 + y] * 0.0625f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i] * b0, b1, om[x][y][g]) * mul;
+            *reinterpret_cast<float4*>(to + 32 * g + 4 * r) = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            to[16 * c + r] = o[c][x][y] * mul;
+            to[16 * c + 8 + r] = o[c][x][2 + y] * mul;
+          }
         }
       }
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 8 * x + 2 * t + (i & 1), up = i >> 1;
-          const int ch = KV4 ? 32 * (c >> 1) + 4 * r + 2 * (c & 1) + up : 16 * c + r + 8 * up;
-          mine[row * D + ch] = KV4 ? o[c][x][i] * (up ? b0 * 0.0625f : b0) * b1 : o[c][x][i];
-        }
-    }
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < heads * D; idx += C::THREADS) {
-    const int row = idx / D, e = idx % D;
-    const float* stat = join + C::ROWS * D + row * C::STATS;
-    float M = NEG_INF, L = 0.f, v = 0.f;
-#pragma unroll
-    for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, stat[w * JOIN]);
+  for (int idx = threadIdx.x; idx < heads * (D / 4); idx += C::THREADS) {
+    const int row = idx / (D / 4), e = idx % (D / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < C::WARPS; ++w) {
-      const float a = sm100::ex2_approx(stat[w * JOIN] - M);
-      L = fmaf(a, stat[w * JOIN + 1], L);
-      v = fmaf(a, join[w * JOIN + idx] + (KV4 ? stat[w * JOIN + 2 + e / 32] : 0.f), v);
+      const float4 u = *reinterpret_cast<const float4*>(join + w * JOIN + row * C::JOIN_ROW + 4 * e);
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
-    const size_t part = (head0 + row) * p.n_split + s;
-    p.part_o[part * D + e] = v / L;
-    if (e == 0) p.part_lse[part] = M + log2f(L);
+    if (whole)
+      reinterpret_cast<uint2*>(p.O + (head0 + row) * D)[e] =
+          make_uint2(sm100::pack_bf16x2(v.x, v.y), sm100::pack_bf16x2(v.z, v.w));
+    else
+      reinterpret_cast<float4*>(p.part_o + (part0 + row) * D)[e] = v;
   }
+  }  // segments
 }
 
-// Joins the splits.  Grid: x < group: the output of query head x of the group; x >= group: the weights of
+// Joins the segments of units that have several.  Grid: x < head blocks: the outputs of a unit; x beyond: the weights of
 // 1024 keys; y: key/value head; z: sequence.
-constexpr int CACHE_FINISH_THREADS = 256;
+constexpr int CACHE_FINISH_THREADS = 512;
 constexpr int CACHE_FINISH_KEYS = 1024;
 
 template <int D>
 __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel(const CacheDecodeParams p) {
-  constexpr int LANES = D / 4, SETS = CACHE_FINISH_THREADS / LANES;  // threads per split's row, splits at a time
+  constexpr int WARPS = CACHE_FINISH_THREADS / 32;
+  __shared__ float s_o[WARPS][D];
   __shared__ float s_lse[32];
-  __shared__ float4 s_o[SETS][LANES];
   cudaGridDependencySynchronize();
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int kvh = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = cache_len(p.kv_lens, b, p.n_cap);
-  const int ns = (len + p.chunk - 1) / p.chunk;
+  const int key0 = ((int)blockIdx.x - p.head_blocks) * CACHE_FINISH_KEYS;
+  if (key0 >= len) return;
   const size_t head0 = (size_t)b * p.H_q + (size_t)kvh * p.group;
-  // base-2 log-sum-exp of a head, by one warp
-  auto head_lse = [&](size_t head) {
-    const float* lse = p.part_lse + head * p.n_split;
+  const int nb = (len + p.block - 1) / p.block;
+  // The segments of unit (kvh, hb): numbers [first, first + n).
+  struct Segments {
+    size_t first;
+    int n;
+  };
+  const long long seq_at = nb ? p.seq_at[b] : 0;
+  const CacheLine line(p, nb ? p.seq_at[p.B] : 1);
+  auto segments = [&](int hb) {
+    const int unit = kvh * p.head_blocks + hb;
+    const long long x = seq_at + (long long)unit * nb;
+    const int c0 = line.cta_of(x), c1 = line.cta_of(x + nb - 1);
+    return Segments{(size_t)b * p.H_kv * p.head_blocks + unit + c0, c1 - c0 + 1};
+  };
+  // Base-2 log-sum-exp of a unit's row, by one warp.
+  auto row_lse = [&](const Segments& g, int row) {
+    const float* lse = p.part_lse + g.first * p.rows + row;
+    if (g.n == 1) return lse[0];
     float M = NEG_INF, L = 0.f;
-    for (int s = lane; s < ns; s += 32) M = fmaxf(M, lse[s]);
+    for (int s = lane; s < g.n; s += 32) M = fmaxf(M, lse[(size_t)s * p.rows]);
 #pragma unroll
     for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     const float m = M == NEG_INF ? 0.f : M;
-    for (int s = lane; s < ns; s += 32) L += exp2f(lse[s] - m);
+    for (int s = lane; s < g.n; s += 32) L += exp2f(lse[(size_t)s * p.rows] - m);
 #pragma unroll
     for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
     return m + log2f(L);
   };
-  if ((int)blockIdx.x < p.group) {
-    const size_t head = head0 + blockIdx.x;
-    if (warp == 0) {
-      const float x = head_lse(head);
-      if (lane == 0) s_lse[0] = x;
+  if (key0 < 0) {
+    const int hb = blockIdx.x, heads = min(p.rows, p.group - hb * p.rows);
+    const size_t first_head = head0 + hb * p.rows;
+    if (nb == 0) {  // no key: 0 and -inf
+      for (int i = threadIdx.x; i < heads * D; i += CACHE_FINISH_THREADS) p.O[first_head * D + i] = __float2bfloat16_rn(0.f);
+      if (p.LSE && threadIdx.x < heads) p.LSE[first_head + threadIdx.x] = NEG_INF;
+      return;
     }
-    __syncthreads();
-    const float l2 = s_lse[0];
-    const int set = threadIdx.x / LANES, e = threadIdx.x % LANES;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = set; s < ns; s += SETS) {
-      const size_t part = head * p.n_split + s;
-      const float w = exp2f(p.part_lse[part] - l2);
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + part * D)[e];
-      a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
-    }
-    s_o[set][e] = a;
-    __syncthreads();
-    if (threadIdx.x < LANES) {
-#pragma unroll
-      for (int i = 1; i < SETS; ++i) {
-        const float4 v = s_o[i][e];
-        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    const Segments g = segments(hb);
+    if (g.n == 1) return;  // written where it was computed
+    // WARPS / rows warps per query head, each with every so-manieth segment; D / 32 channels per lane
+    constexpr int E = D / 32;
+    const int row = warp % p.rows, set = warp / p.rows, sets = WARPS / p.rows;
+    float acc[E] = {};
+    if (row < heads) {
+      const float l2 = row_lse(g, row);
+#pragma unroll 4
+      for (int s = set; s < g.n; s += sets) {
+        const size_t part = (g.first + s) * p.rows + row;
+        const float w = exp2f(p.part_lse[part] - l2);
+        const float* v = p.part_o + part * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(v);
+          acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]), acc[2] = fmaf(w, u.z, acc[2]), acc[3] = fmaf(w, u.w, acc[3]);
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(v);
+          acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]);
+        }
       }
-      reinterpret_cast<uint2*>(p.O + head * D)[e] =
-          make_uint2(sm100::pack_bf16x2(a.x, a.y), sm100::pack_bf16x2(a.z, a.w));
-      if (p.LSE && e == 0) p.LSE[head] = ns ? l2 * 0.69314718055994531f : NEG_INF;
+      if (p.LSE && set == 0 && lane == 0) p.LSE[first_head + row] = l2 * 0.69314718055994531f;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = acc[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * D; i += CACHE_FINISH_THREADS) {
+      float v = 0.f;
+      for (int w = i / D; w < WARPS; w += p.rows) v += s_o[w][i % D];
+      p.O[first_head * D + i] = __float2bfloat16_rn(v);
     }
     return;
   }
-  const int j = ((int)blockIdx.x - p.group) * CACHE_FINISH_KEYS + 4 * threadIdx.x;
-  if (((int)blockIdx.x - p.group) * CACHE_FINISH_KEYS >= len) return;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  const int j = key0 + 2 * threadIdx.x;
+  float w[2] = {0.f, 0.f};
   for (int h0 = 0; h0 < p.group; h0 += 32) {
     const int nh = min(32, p.group - h0);
     __syncthreads();
-    for (int h = warp; h < nh; h += CACHE_FINISH_THREADS / 32) {
-      const float x = head_lse(head0 + h0 + h);
+    for (int h = warp; h < nh; h += WARPS) {
+      const float x = row_lse(segments((h0 + h) / p.rows), (h0 + h) % p.rows);
       if (lane == 0) s_lse[h] = x;
     }
     __syncthreads();
     if (j < len)
+#pragma unroll 4
       for (int h = 0; h < nh; ++h) {
-        const float4 v = *reinterpret_cast<const float4*>(p.scores + (head0 + h0 + h) * p.score_stride + j);
-        w[0] += exp2f(v.x - s_lse[h]), w[1] += exp2f(v.y - s_lse[h]);
-        w[2] += exp2f(v.z - s_lse[h]), w[3] += exp2f(v.w - s_lse[h]);
+        const float2 v = *reinterpret_cast<const float2*>(p.scores + (head0 + h0 + h) * p.score_stride + j);
+        w[0] += exp2f(v.x - s_lse[h]);
+        w[1] += exp2f(v.y - s_lse[h]);
       }
   }
   const size_t at = ((size_t)b * p.H_kv + kvh) * p.n_cap + j;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     if (j + i < len) p.acc_out[at + i] = (p.acc ? p.acc[at + i] : 0.f) + w[i];
 }
 
