@@ -265,6 +265,35 @@ extern "C" int sdpa_decode_acc(const void* Q, const void* K, const void* V, cons
 }
 
 // ------------------------------------------------------------------ weights of a prompt
+namespace {
+
+// Units of 256 keys where every unit has at least eight query tiles to stream past them and there is a unit
+// for every SM; else of 128.
+bool prompt_wide(const sdpa::PromptWeightsParams& p, int) {
+  return (long long)p.group * ((p.n_q + 127) / 128) >= 8 && (long long)p.bkv * ((p.n_kv + 255) / 256) >= 148;
+}
+
+template <int D, int MT>
+int launch_prompt_weights(const void* Q, const void* K, sdpa::PromptWeightsParams p, int batch, cudaStream_t stream) {
+  using Cfg = sdpa::PromptCfg<D, MT>;
+  auto kern = sdpa::sdpa_prompt_weights_kernel<D, MT>;
+  static std::atomic<uint64_t> ready{0};
+  if (int e = allow_smem(kern, Cfg::SMEM_BYTES, ready)) return e;
+  CUtensorMap mq, mk;
+  if (!make_map(&mk, K, D, p.n_kv, p.bkv)) return SDPA_ERR_CUDA;
+  if (p.n_q == 0)
+    mq = mk;  // not read
+  else if (!make_map(&mq, Q, D, p.n_q, batch * p.heads_q))
+    return SDPA_ERR_CUDA;
+  p.n_kt = (p.n_kv + 128 * MT - 1) / (128 * MT);
+  long long grid = (long long)p.bkv * p.n_kt;
+  if (grid > sm_count()) grid = sm_count();
+  kern<<<(unsigned)grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(mq, mk, p);
+  return launched("prompt weights launch");
+}
+
+}  // namespace
+
 extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, const float* acc, float* acc_out, int batch,
                             int heads_q, int heads_kv, int n_q, int n_kv, int n_acc, int d, float scale, int causal,
                             void* stream) {
@@ -275,31 +304,25 @@ extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, cons
   if (batch == 0 || heads_q == 0) return SDPA_OK;
   if (!K || !acc_out || (n_q > 0 && (!Q || !LSE))) return SDPA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(K) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out)) return SDPA_ERR_MISALIGNED;
-  if (!cache_sizes_fit(batch, heads_q, n_q) || !cache_sizes_fit(batch, heads_kv, n_acc) ||
-      (long long)batch * heads_kv > 65535)
-    return SDPA_ERR_UNSUPPORTED;
+  if (!cache_sizes_fit(batch, heads_q, n_q) || !cache_sizes_fit(batch, heads_kv, n_acc)) return SDPA_ERR_UNSUPPORTED;
   if (int e = check_device()) return e;
   sdpa::PromptWeightsParams p = {};
-  p.Q = (const __nv_bfloat16*)Q;
-  p.K = (const __nv_bfloat16*)K;
   p.LSE = LSE;
   p.acc = acc;
   p.acc_out = acc_out;
-  p.H_q = heads_q;
-  p.H_kv = heads_kv;
+  p.heads_q = heads_q;
+  p.heads_kv = heads_kv;
   p.group = heads_q / heads_kv;
   p.n_q = n_q;
   p.n_kv = n_kv;
   p.n_acc = n_acc;
   p.causal = causal;
+  p.bkv = batch * heads_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const dim3 grid((unsigned)((n_kv + 127) / 128), (unsigned)(batch * heads_kv));
   cudaStream_t s = (cudaStream_t)stream;
-  if (d == 64)
-    sdpa::sdpa_prompt_weights_kernel<64><<<grid, 128, 0, s>>>(p);
-  else
-    sdpa::sdpa_prompt_weights_kernel<128><<<grid, 128, 0, s>>>(p);
-  return launched("prompt weights launch");
+  const bool wide = prompt_wide(p, batch);
+  if (d == 64) return wide ? launch_prompt_weights<64, 2>(Q, K, p, batch, s) : launch_prompt_weights<64, 1>(Q, K, p, batch, s);
+  return wide ? launch_prompt_weights<128, 2>(Q, K, p, batch, s) : launch_prompt_weights<128, 1>(Q, K, p, batch, s);
 }
 
 // ------------------------------------------------------------------ eviction

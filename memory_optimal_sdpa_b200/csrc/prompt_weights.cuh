@@ -1,53 +1,402 @@
-// prompt_weights.cuh -- the attention weights of a prompt, summed over its queries.
+// prompt_weights.cuh -- the attention weights of a prompt, summed over its queries, on the sm_100a tensor cores.
+//
+//     w_j = sum over the heads h of a group and the queries i that see key j of 2^(c q_hi . k_j - L_hi)
+//
+// (c = scale log2 e, L the base-2 log-sum-exp): the scores of a prefill once more, but with the sums along the
+// other axis and nothing else kept.  So the keys are the rows of the product, S^T = K Q^T: a thread of the softmax
+// warps owns a key (a TMEM lane), walks over the queries (columns) and keeps the key's sum in registers.  No
+// running maximum, no exchange between threads, no atomics; the order of the sums is fixed.
+//
+// A unit of work is 128 MT keys of one (sequence, key/value head); its queries stream past in tiles of 128, head
+// after head.  MT = 2 halves the L2 traffic of the queries (32 KB per tile of 128 x 256 scores at d = 128;
+// with 128 keys all SMs together would ask for about 9 TB/s), MT = 1 is for few queries, where the keys are the
+// stream.  What bounds it: for many queries the exponentials (16 per clock and SM on the MUFU unit, so 1024
+// clocks for 128 x 128 scores, against 256 for the MMA at d = 128); every POLY_EVERY-th pair takes them on the FMA
+// pipe instead.  For few queries HBM (the keys).
+//
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 log-sum-exps into shared memory, 3 idle, then softmax groups of
+// four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
+// groups of turn i mod TURNS (one group for each 128 keys), so that a stage always meets the same groups and they
+// wait for each of its phases in order: a parity cannot be mistaken for a later one.  At the end of a unit the group that had its last
+// tile collects the other turns' sums through shared memory (monotonic counters, two slots) and stores.
 #pragma once
 
 #include "kv4.cuh"
+#include "prefill_bf16.cuh"
 
 namespace sdpa {
 
 struct PromptWeightsParams {
-  const __nv_bfloat16* Q;  // [B, Hq, n_q, D]
-  const __nv_bfloat16* K;  // [B, Hkv, n_kv, D]
-  const float* LSE;        // [B, Hq, n_q]
+  const float* LSE;        // [B, Hq, n_q], natural
   const float* acc;        // [B, Hkv, n_acc] or null
   float* acc_out;
-  int H_q, H_kv, group, n_q, n_kv, n_acc, causal;
+  int heads_q, heads_kv, group, n_q, n_kv, n_acc, causal;
+  int bkv, n_kt;           // B Hkv; key units per (sequence, key/value head)
   float scale_log2;
 };
 
-// One thread per key, query rows staged in shared memory.
-template <int D>
-__global__ void __launch_bounds__(128) sdpa_prompt_weights_kernel(const PromptWeightsParams p) {
-  constexpr int TILE = 32;
-  __shared__ float s_q[TILE][D];
-  __shared__ float s_lse[TILE];
-  const int b = blockIdx.y / p.H_kv, kvh = blockIdx.y % p.H_kv;
-  const int j = blockIdx.x * 128 + threadIdx.x;
-  const size_t bkv = blockIdx.y;
-  float k[D];
-  for (int e = 0; e < D; ++e) k[e] = j < p.n_kv ? __bfloat162float(p.K[(bkv * p.n_kv + j) * D + e]) * p.scale_log2 : 0.f;
-  float w = 0.f;
-  for (int h = 0; h < p.group; ++h) {
-    const size_t head = (size_t)b * p.H_q + kvh * p.group + h;
-    for (int i0 = 0; i0 < p.n_q; i0 += TILE) {
-      const int n = min(TILE, p.n_q - i0);
-      __syncthreads();
-      for (int i = threadIdx.x; i < n * D; i += 128)
-        s_q[i / D][i % D] = __bfloat162float(p.Q[(head * p.n_q + i0) * D + i]);
-      if (threadIdx.x < n) s_lse[threadIdx.x] = p.LSE[head * p.n_q + i0 + threadIdx.x];
-      __syncthreads();
-      float part = 0.f;
-      for (int i = 0; i < n; ++i) {
-        if (p.causal && j > i0 + i + p.n_kv - p.n_q) continue;
-        if (fabsf(s_lse[i]) == __int_as_float(0x7f800000)) continue;
-        float d = 0.f;
-        for (int e = 0; e < D; ++e) d = fmaf(k[e], s_q[i][e], d);
-        part += exp2f(d - s_lse[i] * 1.4426950408889634f);
+#ifndef SDPA_PROMPT_POLY_EVERY
+#define SDPA_PROMPT_POLY_EVERY 4
+#endif
+#ifndef SDPA_PROMPT_GROUPS
+#define SDPA_PROMPT_GROUPS 2  // MT = 2
+#endif
+
+template <int D, int MT>
+struct PromptCfg {
+  static constexpr int TILE_BYTES = 128 * D * 2;
+  static constexpr int BLOCK_BYTES = 128 * 64 * 2;  // one 64-channel swizzle block
+  static constexpr int KSLOT = D == 128 ? (MT == 2 ? 1 : 3) : (MT == 2 ? 3 : 6);
+  static constexpr int QSLOT = D == 128 ? (MT == 2 ? 4 : 3) : (MT == 2 ? 6 : 6);
+  static constexpr int NSTAGE = 512 / (128 * MT);
+  static constexpr int K_OFF = 0;
+  static constexpr int Q_OFF = KSLOT * MT * TILE_BYTES;
+  static constexpr int GROUPS = MT == 2 ? SDPA_PROMPT_GROUPS : 2;
+  static constexpr int TURNS = GROUPS / MT;
+  static_assert(NSTAGE % TURNS == 0, "a stage belongs to one turn");
+  static_assert(TURNS <= 2, "the sums a turn sends are collected by one other turn, so in order");
+  static constexpr int LSE_OFF = Q_OFF + QSLOT * TILE_BYTES;  // [NSTAGE][128]
+  static constexpr int FLAG_OFF = LSE_OFF + NSTAGE * 128 * 4;  // [NSTAGE]: whether one of them is infinite
+  static constexpr int CNT_OFF = FLAG_OFF + 16;                // [2][GROUPS * 4]: sums sent, sums collected
+  static constexpr int SUM_OFF = CNT_OFF + 2 * GROUPS * 4 * 4;                 // [2][TURNS][MT * 128]
+  static constexpr int BAR_OFF = SUM_OFF + 2 * TURNS * MT * 128 * 4;
+  // k_full, k_empty, q_full, q_empty, s_full, s_free, drain
+  static constexpr int NBAR = 2 * KSLOT + 2 * QSLOT + 2 * NSTAGE + 1;
+  static constexpr int SMEM_BYTES = BAR_OFF + NBAR * 8 + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
+  static constexpr int THREADS = 128 + 128 * GROUPS;
+};
+
+// 2^x for a pair on the FMA pipe, -inf <= x <= 64: as sm100::exp2_poly2 (x = j + f, 2^f by a polynomial, j into the
+// exponent), with a degree-5 polynomial (Remez exchange on [-1/2, 1/2]: relative error 7.5e-8, in fp32 2.1e-7, as
+// ex2.approx has): these weights are results, not rounded to bf16 afterwards.  Below 2^-125 it gives about 2^-125.
+__device__ __forceinline__ float2 exp2_fine2(float2 x) {
+  using namespace sm100;
+  constexpr float SHIFT = 12582912.0f;  // 1.5 * 2^23
+  x.x = fmaxf(x.x, -125.f);
+  x.y = fmaxf(x.y, -125.f);
+  const float2 t = fadd2(x, make_float2(SHIFT, SHIFT));
+  const float2 r = fadd2(t, make_float2(-SHIFT, -SHIFT));
+  const float2 f = ffma2(r, make_float2(-1.f, -1.f), x);
+  float2 q = ffma2(make_float2(0x1.5c08e6p-10f, 0x1.5c08e6p-10f), f, make_float2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+  q = ffma2(q, f, make_float2(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
+  q = ffma2(q, f, make_float2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+  q = ffma2(q, f, make_float2(0x1.62e428p-1f, 0x1.62e428p-1f));
+  q = ffma2(q, f, make_float2(0x1.000002p+0f, 0x1.000002p+0f));
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// The sum of 2^(s c2 - L) over 32 columns.  first: columns below it are masked (0 and less: none).
+// EVERY > 0: every EVERY-th pair on the FMA pipe, no masks and only finite exponents; 0: the form for both.
+template <int EVERY>
+__device__ __forceinline__ float prompt_chunk(const uint32_t (&s)[32], float c2, const float4* L, int first) {
+  using namespace sm100;
+  float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+  const float2 cc = make_float2(c2, c2);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 l = L[i];  // minus the log-sum-exps
+    const float2 x0 = ffma2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), cc, make_float2(l.x, l.y));
+    const float2 x1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cc, make_float2(l.z, l.w));
+    float2 e0, e1;
+    if (EVERY > 0 && (2 * i) % (EVERY > 0 ? EVERY : 1) == 0)
+      e0 = exp2_fine2(x0);
+    else
+      e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+    if (EVERY > 0 && (2 * i + 1) % (EVERY > 0 ? EVERY : 1) == 0)
+      e1 = exp2_fine2(x1);
+    else
+      e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+    if (EVERY == 0) {  // the masked form
+      if (4 * i < first) e0.x = 0.f;
+      if (4 * i + 1 < first) e0.y = 0.f;
+      if (4 * i + 2 < first) e1.x = 0.f;
+      if (4 * i + 3 < first) e1.y = 0.f;
+    }
+    a0 = fadd2(a0, e0);
+    a1 = fadd2(a1, e1);
+  }
+  const float2 a = fadd2(a0, a1);
+  return a.x + a.y;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
+    sdpa_prompt_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                               const PromptWeightsParams p) {
+  using C = PromptCfg<D, MT>;
+  using namespace sm100;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sK = smem + C::K_OFF;
+  uint8_t* sQ = smem + C::Q_OFF;
+  float* sL = (float*)(smem + C::LSE_OFF);
+  volatile int* sF = (volatile int*)(smem + C::FLAG_OFF);
+  uint32_t* sent = (uint32_t*)(smem + C::CNT_OFF);  // [turn][key warp]
+  uint32_t* collected = sent + 4 * C::GROUPS;
+  float* sums = (float*)(smem + C::SUM_OFF);
+  uint64_t* k_full = (uint64_t*)(smem + C::BAR_OFF);
+  uint64_t* k_empty = k_full + C::KSLOT;
+  uint64_t* q_full = k_empty + C::KSLOT;
+  uint64_t* q_empty = q_full + C::QSLOT;
+  uint64_t* s_full = q_empty + C::QSLOT;
+  uint64_t* s_free = s_full + C::NSTAGE;
+  uint64_t* drain = s_free + C::NSTAGE;
+  uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::KSLOT; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::QSLOT; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < C::NSTAGE; ++i) {
+      mbar_init(&s_full[i], 2);            // the product and the log-sum-exps
+      mbar_init(&s_free[i], 4 * MT);       // the warps that read the stage
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < 8 * C::GROUPS; ++i) sent[i] = 0;
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  bool timed_out = false;
+  const bool tmem_bad = tmem_alloc_bad(tmem);  // debug builds only
+
+  // Units: key unit by key unit, the (sequence, key/value head) slices side by side; under a causal mask the first
+  // keys have the most queries, so the heaviest come first, and successive rounds are dealt in alternating directions.
+  const int n_units = p.bkv * p.n_kt;
+  auto unit_of = [&](int k) {
+    const int G = (int)gridDim.x, b = (int)blockIdx.x;
+    return (k & 1) ? (k + 1) * G - 1 - b : k * G + b;
+  };
+  const int off = p.n_kv - p.n_q;
+  const int n_qt = (p.n_q + 127) / 128;
+  struct Unit {
+    int bkv, key0, qt0;  // first key; query tiles [qt0, n_qt) of every head of the group
+  };
+  auto unit_at = [&](int u) {
+    Unit g;
+    g.bkv = u % p.bkv;
+    g.key0 = (u / p.bkv) * 128 * MT;
+    const int first = p.causal ? g.key0 - off : 0;  // the first query that sees the unit's first key
+    g.qt0 = first > 0 ? first / 128 : 0;
+    return g;
+  };
+  auto q_head = [&](int bkv, int h) {  // row of [B Hq]
+    return (bkv / p.heads_kv) * p.heads_q + (bkv % p.heads_kv) * p.group + h;
+  };
+
+  if (tmem_bad) {
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      int nk = 0, nq = 0;  // units and query tiles loaded
+      bool ok = true;
+      for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
+        const Unit g = unit_at(u);
+        if (g.qt0 >= n_qt) continue;
+        const int ks = nk % C::KSLOT;
+        if (!(ok = mbar_wait_bounded(&k_empty[ks], ((uint32_t)(nk / C::KSLOT) & 1u) ^ 1u, abort_flag, &timed_out))) break;
+        mbar_arrive_expect_tx(&k_full[ks], MT * C::TILE_BYTES);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sK + (ks * MT + m) * C::TILE_BYTES + c * C::BLOCK_BYTES, &tmK, &k_full[ks], 64 * c, g.key0 + 128 * m,
+                        g.bkv);
+        ++nk;
+        for (int h = 0; ok && h < p.group; ++h)
+          for (int qt = g.qt0; qt < n_qt; ++qt) {
+            const int qs = nq % C::QSLOT;
+            if (!(ok = mbar_wait_bounded(&q_empty[qs], ((uint32_t)(nq / C::QSLOT) & 1u) ^ 1u, abort_flag, &timed_out))) break;
+            mbar_arrive_expect_tx(&q_full[qs], C::TILE_BYTES);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sQ + qs * C::TILE_BYTES + c * C::BLOCK_BYTES, &tmQ, &q_full[qs], 64 * c, 128 * qt, q_head(g.bkv, h));
+            ++nq;
+          }
       }
-      w += part;
+      if (*abort_flag) {  // let the copies in flight land before the CTA exits
+        for (int i = nk > C::KSLOT ? nk - C::KSLOT : 0; i < nk; ++i)
+          mbar_wait_drain(&k_full[i % C::KSLOT], (uint32_t)(i / C::KSLOT) & 1u);
+        for (int i = nq > C::QSLOT ? nq - C::QSLOT : 0; i < nq; ++i)
+          mbar_wait_drain(&q_full[i % C::QSLOT], (uint32_t)(i / C::QSLOT) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      int nk = 0, nq = 0;
+      bool ok = true;
+      for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
+        const Unit g = unit_at(u);
+        if (g.qt0 >= n_qt) continue;
+        const int ks = nk % C::KSLOT;
+        if (!(ok = mbar_wait_bounded(&k_full[ks], (uint32_t)(nk / C::KSLOT) & 1u, abort_flag, &timed_out))) break;
+        const int tiles = p.group * (n_qt - g.qt0);
+        for (int i = 0; i < tiles; ++i, ++nq) {
+          const int qs = nq % C::QSLOT, st = nq % C::NSTAGE;
+          if (!(ok = mbar_wait_bounded(&q_full[qs], (uint32_t)(nq / C::QSLOT) & 1u, abort_flag, &timed_out) &&
+                     mbar_wait_bounded(&s_free[st], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag, &timed_out)))
+            break;
+          tc_fence_after_sync();  // the stage's last reads come before this product
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * C::BLOCK_BYTES) + (kk & 3) * 32;
+              mma_ss(tmem + (uint32_t)((st * MT + m) * 128), dK + (uint64_t)(((ks * MT + m) * C::TILE_BYTES + o) >> 4),
+                     dQ + (uint64_t)((qs * C::TILE_BYTES + o) >> 4), id, kk > 0 ? 1u : 0u);
+            }
+          tc_commit(&s_full[st]);
+          tc_commit(&q_empty[qs]);
+        }
+        if (!ok) break;
+        tc_commit(&k_empty[ks]);
+        ++nk;
+      }
+      tc_commit(drain);
+      mbar_wait_drain(drain, 0);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ log-sum-exps, negated, base 2
+    int nq = 0;
+    bool ok = true;
+    for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
+      const Unit g = unit_at(u);
+      for (int h = 0; ok && h < p.group; ++h) {
+        const float* L = p.LSE + (size_t)q_head(g.bkv, h) * p.n_q;
+        for (int qt = g.qt0; qt < n_qt; ++qt, ++nq) {
+          const int st = nq % C::NSTAGE;
+          float v[4];
+          bool none = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 128 * qt + 32 * i + lane;
+            const float x = row < p.n_q ? -1.4426950408889634f * __ldg(L + row) : -__int_as_float(0x7f800000);
+            v[i] = x == __int_as_float(0x7f800000) ? -x : x;  // a query that sees no key (LSE -inf) adds nothing
+            none |= v[i] == -__int_as_float(0x7f800000);
+          }
+          none = __any_sync(0xffffffffu, none);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_free[st], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag,
+                                                         &timed_out));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sL[st * 128 + 32 * i + lane] = v[i];
+          if (lane == 0) sF[st] = none;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_full[st]);
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax groups
+    const int grp = (warp - 4) >> 2, q4 = warp & 3;
+    const int m = grp % MT, turn = grp / MT, kw = 4 * m + q4;  // kw: which 32 keys of the unit
+    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const float c2 = p.scale_log2;
+    int nq = 0;             // query tiles of the units so far
+    uint32_t n_sent[C::TURNS] = {};  // sums that each turn has sent for a key warp
+    bool ok = true;
+    for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
+      const Unit g = unit_at(u);
+      const int tiles_head = n_qt - g.qt0 > 0 ? n_qt - g.qt0 : 0, tiles = p.group * tiles_head;
+      const int key = g.key0 + 32 * kw + lane;
+      const int warp_last = g.key0 + 32 * kw + 31;  // the warp's last key: masks the most
+      float w = 0.f;
+      const int skip = (turn - nq % C::TURNS + C::TURNS) % C::TURNS;  // this turn's first tile of the unit
+      int qt = g.qt0 + (tiles_head ? skip % tiles_head : 0);
+      for (int i = skip; i < tiles; i += C::TURNS) {
+        const int st = (nq + i) % C::NSTAGE;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&s_full[st], (uint32_t)((nq + i) / C::NSTAGE) & 1u, abort_flag, &timed_out));
+        if (!ok) break;
+        tc_fence_after_sync();
+        const int row0 = 128 * qt;
+        const int cols = p.n_q - row0 < 128 ? p.n_q - row0 : 128;
+        const uint32_t ta = tmem + (uint32_t)((st * MT + m) * 128) + lane_base;
+        const float4* L = reinterpret_cast<const float4*>(sL + st * 128);
+        // query row0 + c sees the key iff c >= key - off - row0
+        const int first = p.causal ? key - off - row0 : 0;
+        // the exponential on the FMA pipe does not reach 0
+        const bool masked = sF[st] || (p.causal && warp_last - off - row0 > 0);
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(ta, s[0]);
+        float part = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c < cols) {
+            tmem_wait_ld();
+            reg_fence(s[c & 1]);
+            if (c < 3 && 32 * (c + 1) < cols) tmem_ld_32x32b_x32(ta + (uint32_t)(32 * (c + 1)), s[(c + 1) & 1]);
+            part += masked ? prompt_chunk<0>(s[c & 1], c2, L + 8 * c, first - 32 * c)
+                           : prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[c & 1], c2, L + 8 * c, 0);
+          }
+        }
+        w += part;
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[st]);
+        qt += C::TURNS;
+        while (qt >= n_qt) qt -= tiles_head;  // on to the next head
+      }
+      if (!ok) break;
+      const int last_turn = tiles > 0 ? (nq + tiles - 1) % C::TURNS : 0;
+#pragma unroll
+      for (int t = 0; t < C::TURNS; ++t) {
+        if (t == last_turn || (t - nq % C::TURNS + C::TURNS) % C::TURNS >= tiles) continue;  // no sum to send
+        float* slot = sums + ((n_sent[t] & 1) * C::TURNS + t) * (MT * 128) + 32 * kw + lane;
+        if (turn == t) {  // the slot's last sum has been collected
+          ok = __all_sync(0xffffffffu, count_wait_bounded(&collected[t * 4 * MT + kw], n_sent[t] < 2 ? 0 : n_sent[t] - 1,
+                                                          abort_flag, &timed_out));
+          if (!ok) break;
+          *slot = w;
+          __syncwarp();
+          if (lane == 0) red_release_add(&sent[t * 4 * MT + kw], 1);
+        } else if (turn == last_turn) {
+          ok = __all_sync(0xffffffffu, count_wait_bounded(&sent[t * 4 * MT + kw], n_sent[t] + 1, abort_flag, &timed_out));
+          if (!ok) break;
+          w += *slot;
+          __syncwarp();
+          if (lane == 0) red_release_add(&collected[t * 4 * MT + kw], 1);
+        }
+        ++n_sent[t];
+      }
+      nq += tiles;
+      if (!ok || turn != last_turn) continue;
+      if (key < p.n_kv) {
+        const size_t at = (size_t)g.bkv * p.n_acc + key;
+        p.acc_out[at] = (p.acc ? p.acc[at] : 0.f) + w;
+      }
     }
   }
-  if (j < p.n_kv) p.acc_out[bkv * p.n_acc + j] = (p.acc ? p.acc[bkv * p.n_acc + j] : 0.f) + w;
+
+  if (timed_out) record_error(6 /* SDPA_ERR_DEVICE_TIMEOUT */);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 }  // namespace sdpa

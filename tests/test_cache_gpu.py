@@ -319,6 +319,9 @@ PROMPT = [  # B, Hq, Hkv, n_q, n_kv, d, causal
     (1, 1, 1, 1, 1, 64, False), (1, 1, 1, 1, 1, 128, True), (2, 3, 1, 1, 129, 128, True), (1, 2, 2, 128, 128, 64, True),
     (1, 4, 2, 127, 255, 128, True), (2, 2, 1, 300, 100, 64, True), (1, 6, 2, 65, 1000, 128, False), (1, 5, 1, 257, 257, 128, True),
     (3, 2, 2, 64, 513, 64, True), (1, 8, 2, 1024, 1024, 128, True), (1, 2, 1, 700, 640, 64, False), (1, 1, 1, 129, 2, 128, True),
+    # several units per block with one, two, an odd and many query tiles each, for narrow and wide units
+    (4, 8, 8, 100, 1100, 64, True), (4, 8, 8, 200, 1000, 128, False), (2, 24, 8, 380, 1500, 64, True), (2, 6, 2, 1300, 6000, 128, True),
+    (2, 16, 8, 520, 2500, 64, True), (2, 16, 8, 600, 2600, 128, False), (4, 20, 4, 300, 2400, 128, True),
 ]
 
 
