@@ -14,7 +14,7 @@
 // clocks for 128 x 128 scores, against 256 for the MMA at d = 128); every POLY_EVERY-th pair takes them on the FMA
 // pipe instead.  For few queries HBM (the keys).
 //
-// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 log-sum-exps into shared memory, 3 idle, then softmax groups of
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 and 3 log-sum-exps into shared memory, then softmax groups of
 // four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
 // groups of turn i mod TURNS (one group for each 128 keys), so that a stage always meets the same groups and they
 // wait for each of its phases in order: a parity cannot be mistaken for a later one.  At the end of a unit the group that had its last
@@ -39,7 +39,7 @@ struct PromptWeightsParams {
 #define SDPA_PROMPT_POLY_EVERY 4
 #endif
 #ifndef SDPA_PROMPT_GROUPS
-#define SDPA_PROMPT_GROUPS 2  // MT = 2
+#define SDPA_PROMPT_GROUPS 4
 #endif
 
 template <int D, int MT>
@@ -51,17 +51,17 @@ struct PromptCfg {
   static constexpr int NSTAGE = 512 / (128 * MT);
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KSLOT * MT * TILE_BYTES;
-  static constexpr int GROUPS = MT == 2 ? SDPA_PROMPT_GROUPS : 2;
+  static constexpr int GROUPS = SDPA_PROMPT_GROUPS;
   static constexpr int TURNS = GROUPS / MT;
   static_assert(NSTAGE % TURNS == 0, "a stage belongs to one turn");
-  static_assert(TURNS <= 2, "the sums a turn sends are collected by one other turn, so in order");
   static constexpr int LSE_OFF = Q_OFF + QSLOT * TILE_BYTES;  // [NSTAGE][128]
   static constexpr int FLAG_OFF = LSE_OFF + NSTAGE * 128 * 4;  // [NSTAGE]: whether one of them is infinite
-  static constexpr int CNT_OFF = FLAG_OFF + 16;                // [2][GROUPS * 4]: sums sent, sums collected
-  static constexpr int SUM_OFF = CNT_OFF + 2 * GROUPS * 4 * 4;                 // [2][TURNS][MT * 128]
-  static constexpr int BAR_OFF = SUM_OFF + 2 * TURNS * MT * 128 * 4;
+  static constexpr int CNT_OFF = FLAG_OFF + 16;                // [2][TURNS][TURNS][MT * 4]: sums sent, sums collected
+  static constexpr int CNT = TURNS * TURNS * MT * 4;
+  static constexpr int SUM_OFF = CNT_OFF + 2 * CNT * 4;        // [2][TURNS][TURNS][MT * 128]
+  static constexpr int BAR_OFF = SUM_OFF + 2 * TURNS * TURNS * MT * 128 * 4;
   // k_full, k_empty, q_full, q_empty, s_full, s_free, drain
-  static constexpr int NBAR = 2 * KSLOT + 2 * QSLOT + 2 * NSTAGE + 1;
+  static constexpr int NBAR = 2 * KSLOT + 2 * QSLOT + 2 * NSTAGE * MT + 1;
   static constexpr int SMEM_BYTES = BAR_OFF + NBAR * 8 + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
   static constexpr int THREADS = 128 + 128 * GROUPS;
@@ -87,15 +87,15 @@ __device__ __forceinline__ float2 exp2_fine2(float2 x) {
                      __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// The sum of 2^(s c2 - L) over 32 columns.  first: columns below it are masked (0 and less: none).
+// The sum of 2^(s c2 - L) over 16 columns.  first: columns below it are masked (0 and less: none).
 // EVERY > 0: every EVERY-th pair on the FMA pipe, no masks and only finite exponents; 0: the form for both.
 template <int EVERY>
-__device__ __forceinline__ float prompt_chunk(const uint32_t (&s)[32], float c2, const float4* L, int first) {
+__device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2, const float4* L, int first, float2 sum) {
   using namespace sm100;
-  float2 a0 = make_float2(0.f, 0.f), a1 = make_float2(0.f, 0.f);
+  float2 a0 = make_float2(0.f, 0.f), a1 = a0;
   const float2 cc = make_float2(c2, c2);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const float4 l = L[i];  // minus the log-sum-exps
     const float2 x0 = ffma2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), cc, make_float2(l.x, l.y));
     const float2 x1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cc, make_float2(l.z, l.w));
@@ -117,8 +117,7 @@ __device__ __forceinline__ float prompt_chunk(const uint32_t (&s)[32], float c2,
     a0 = fadd2(a0, e0);
     a1 = fadd2(a1, e1);
   }
-  const float2 a = fadd2(a0, a1);
-  return a.x + a.y;
+  return fadd2(sum, fadd2(a0, a1));
 }
 
 template <int D, int MT>
@@ -133,16 +132,16 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
   uint8_t* sQ = smem + C::Q_OFF;
   float* sL = (float*)(smem + C::LSE_OFF);
   volatile int* sF = (volatile int*)(smem + C::FLAG_OFF);
-  uint32_t* sent = (uint32_t*)(smem + C::CNT_OFF);  // [turn][key warp]
-  uint32_t* collected = sent + 4 * C::GROUPS;
+  uint32_t* sent = (uint32_t*)(smem + C::CNT_OFF);  // [from turn][to turn][key warp]
+  uint32_t* collected = sent + C::CNT;
   float* sums = (float*)(smem + C::SUM_OFF);
   uint64_t* k_full = (uint64_t*)(smem + C::BAR_OFF);
   uint64_t* k_empty = k_full + C::KSLOT;
   uint64_t* q_full = k_empty + C::KSLOT;
   uint64_t* q_empty = q_full + C::QSLOT;
   uint64_t* s_full = q_empty + C::QSLOT;
-  uint64_t* s_free = s_full + C::NSTAGE;
-  uint64_t* drain = s_free + C::NSTAGE;
+  uint64_t* s_free = s_full + C::NSTAGE * MT;  // [stage][128 keys]
+  uint64_t* drain = s_free + C::NSTAGE * MT;
   uint32_t* tmem_slot = (uint32_t*)(drain + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,12 +155,12 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
-    for (int i = 0; i < C::NSTAGE; ++i) {
-      mbar_init(&s_full[i], 2);            // the product and the log-sum-exps
-      mbar_init(&s_free[i], 4 * MT);       // the warps that read the stage
+    for (int i = 0; i < C::NSTAGE * MT; ++i) {
+      mbar_init(&s_full[i], 2);  // the product and the log-sum-exps
+      mbar_init(&s_free[i], 4);  // the warps of the group that reads it
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < 8 * C::GROUPS; ++i) sent[i] = 0;
+    for (int i = 0; i < 2 * C::CNT; ++i) sent[i] = 0;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -254,19 +253,22 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         const int tiles = p.group * (n_qt - g.qt0);
         for (int i = 0; i < tiles; ++i, ++nq) {
           const int qs = nq % C::QSLOT, st = nq % C::NSTAGE;
-          if (!(ok = mbar_wait_bounded(&q_full[qs], (uint32_t)(nq / C::QSLOT) & 1u, abort_flag, &timed_out) &&
-                     mbar_wait_bounded(&s_free[st], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag, &timed_out)))
-            break;
-          tc_fence_after_sync();  // the stage's last reads come before this product
+          if (!(ok = mbar_wait_bounded(&q_full[qs], (uint32_t)(nq / C::QSLOT) & 1u, abort_flag, &timed_out))) break;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int m = 0; m < MT; ++m) {
+            if (!(ok = ok && mbar_wait_bounded(&s_free[st * MT + m], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag,
+                                               &timed_out)))
+              break;
+            tc_fence_after_sync();  // the stage's last reads come before this product
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t o = ((kk >> 2) * C::BLOCK_BYTES) + (kk & 3) * 32;
               mma_ss(tmem + (uint32_t)((st * MT + m) * 128), dK + (uint64_t)(((ks * MT + m) * C::TILE_BYTES + o) >> 4),
                      dQ + (uint64_t)((qs * C::TILE_BYTES + o) >> 4), id, kk > 0 ? 1u : 0u);
             }
-          tc_commit(&s_full[st]);
+            tc_commit(&s_full[st * MT + m]);
+          }
+          if (!ok) break;
           tc_commit(&q_empty[qs]);
         }
         if (!ok) break;
@@ -276,36 +278,73 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       tc_commit(drain);
       mbar_wait_drain(drain, 0);
     }
-  } else if (warp == 2) {
+  } else if (warp <= 3) {
     // ------------------------------------------------------------------ log-sum-exps, negated, base 2
-    int nq = 0;
-    bool ok = true;
-    for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
-      const Unit g = unit_at(u);
-      for (int h = 0; ok && h < p.group; ++h) {
-        const float* L = p.LSE + (size_t)q_head(g.bkv, h) * p.n_q;
-        for (int qt = g.qt0; qt < n_qt; ++qt, ++nq) {
-          const int st = nq % C::NSTAGE;
-          float v[4];
-          bool none = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 128 * qt + 32 * i + lane;
-            const float x = row < p.n_q ? -1.4426950408889634f * __ldg(L + row) : -__int_as_float(0x7f800000);
-            v[i] = x == __int_as_float(0x7f800000) ? -x : x;  // a query that sees no key (LSE -inf) adds nothing
-            none |= v[i] == -__int_as_float(0x7f800000);
-          }
-          none = __any_sync(0xffffffffu, none);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_free[st], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag,
-                                                         &timed_out));
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sL[st * 128 + 32 * i + lane] = v[i];
-          if (lane == 0) sF[st] = none;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[st]);
+    // Two warps take turns; each has its next tile's values on the way while it waits for a stage.
+    struct Walk {  // over the query tiles of this CTA
+      int k, h, qt;
+      Unit g;
+    };
+    auto settle = [&](Walk& x) {  // on to a tile that exists; false: none is left
+      for (;;) {
+        const int u = unit_of(x.k);
+        if (u >= n_units) return false;
+        if (x.qt < 0) {
+          x.g = unit_at(u);
+          x.qt = x.g.qt0;
+          x.h = 0;
         }
+        if (x.qt >= n_qt && x.g.qt0 < n_qt) {
+          x.qt = x.g.qt0;
+          ++x.h;
+        }
+        if (x.qt < n_qt && x.h < p.group) return true;
+        ++x.k;
+        x.qt = -1;
       }
+    };
+    auto next = [&](Walk& x) {
+      ++x.qt;
+      return settle(x);
+    };
+    auto fetch = [&](const Walk& x, float (&v)[4]) {
+      const float* L = p.LSE + (size_t)q_head(x.g.bkv, x.h) * p.n_q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 128 * x.qt + 32 * i + lane;
+        v[i] = row < p.n_q ? __ldg(L + row) : -__int_as_float(0x7f800000);
+      }
+    };
+    int x_rows = 0, next_rows = 0;  // rows of the tile that exist
+    Walk x = {0, 0, -1, {}};
+    bool more = settle(x);
+    if (more && warp == 3) more = next(x);
+    float v[4];
+    if (more) fetch(x, v), x_rows = p.n_q - 128 * x.qt;
+    for (int nq = warp - 2; more; nq += 2) {
+      float next_v[4] = {};
+      more = next(x) && next(x);
+      if (more) fetch(x, next_v), next_rows = p.n_q - 128 * x.qt;
+      const int st = nq % C::NSTAGE;
+      bool free = true;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        free = free && mbar_wait_bounded(&s_free[st * MT + m], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag, &timed_out);
+      if (!__all_sync(0xffffffffu, free)) break;
+      bool none = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y = -1.4426950408889634f * v[i];
+        v[i] = y == __int_as_float(0x7f800000) ? -y : y;  // a query that sees no key (LSE -inf) adds nothing
+        none |= v[i] == -__int_as_float(0x7f800000) && 32 * i + lane < x_rows;
+        sL[st * 128 + 32 * i + lane] = v[i];
+        v[i] = next_v[i];
+      }
+      x_rows = next_rows;
+      none = __any_sync(0xffffffffu, none);
+      if (lane == 0) sF[st] = none;
+      __syncwarp();
+      if (lane < MT) mbar_arrive(&s_full[st * MT + lane]);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax groups
@@ -314,20 +353,22 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
     const float c2 = p.scale_log2;
     int nq = 0;             // query tiles of the units so far
-    uint32_t n_sent[C::TURNS] = {};  // sums that each turn has sent for a key warp
+    uint32_t n_sent[C::TURNS] = {}, n_got[C::TURNS] = {};  // sums sent to and collected from each turn
     bool ok = true;
     for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
       const Unit g = unit_at(u);
       const int tiles_head = n_qt - g.qt0 > 0 ? n_qt - g.qt0 : 0, tiles = p.group * tiles_head;
       const int key = g.key0 + 32 * kw + lane;
       const int warp_last = g.key0 + 32 * kw + 31;  // the warp's last key: masks the most
+      const size_t at = (size_t)g.bkv * p.n_acc + key;
+      const float before = p.acc && key < p.n_kv ? p.acc[at] : 0.f;  // early: its latency is a unit's work away
       float w = 0.f;
       const int skip = (turn - nq % C::TURNS + C::TURNS) % C::TURNS;  // this turn's first tile of the unit
       int qt = g.qt0 + (tiles_head ? skip % tiles_head : 0);
       for (int i = skip; i < tiles; i += C::TURNS) {
         const int st = (nq + i) % C::NSTAGE;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&s_full[st], (uint32_t)((nq + i) / C::NSTAGE) & 1u, abort_flag, &timed_out));
+                        mbar_wait_bounded(&s_full[st * MT + m], (uint32_t)((nq + i) / C::NSTAGE) & 1u, abort_flag, &timed_out));
         if (!ok) break;
         tc_fence_after_sync();
         const int row0 = 128 * qt;
@@ -338,54 +379,73 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         const int first = p.causal ? key - off - row0 : 0;
         // the exponential on the FMA pipe does not reach 0
         const bool masked = sF[st] || (p.causal && warp_last - off - row0 > 0);
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(ta, s[0]);
-        float part = 0.f;
+        float2 part = make_float2(0.f, 0.f);
+        uint32_t s[2][16];
+        tmem_ld_32x32b_x16(ta, s[0]);
+        if (!masked && cols == 128) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c < cols) {
+          for (int c = 0; c < 8; ++c) {
             tmem_wait_ld();
             reg_fence(s[c & 1]);
-            if (c < 3 && 32 * (c + 1) < cols) tmem_ld_32x32b_x32(ta + (uint32_t)(32 * (c + 1)), s[(c + 1) & 1]);
-            part += masked ? prompt_chunk<0>(s[c & 1], c2, L + 8 * c, first - 32 * c)
-                           : prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[c & 1], c2, L + 8 * c, 0);
+            if (c < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + 1)), s[(c + 1) & 1]);
+            part = prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[c & 1], c2, L + 4 * c, 0, part);
           }
+        } else {
+#pragma unroll 1
+          for (int c = 0; 16 * c < cols; c += 2)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              tmem_wait_ld();
+              reg_fence(s[y]);
+              if (c + y < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + y + 1)), s[y ^ 1]);
+              if (masked || 16 * (c + y + 1) > cols)
+                part = prompt_chunk<0>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), part);
+              else
+                part = prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[y], c2, L + 4 * (c + y), 0, part);
+            }
+          tmem_wait_ld();  // the load ahead of the last columns
         }
-        w += part;
+        w += part.x + part.y;
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[st]);
+        if (lane == 0) mbar_arrive(&s_free[st * MT + m]);
         qt += C::TURNS;
         while (qt >= n_qt) qt -= tiles_head;  // on to the next head
       }
       if (!ok) break;
       const int last_turn = tiles > 0 ? (nq + tiles - 1) % C::TURNS : 0;
+      // Between any two turns the sums go in order, through two slots and two monotonic counters of their own.
+      auto channel = [&](int from, int to) { return (from * C::TURNS + to) * (4 * MT) + kw; };
+      if (turn != last_turn) {
+        if (skip < tiles) {
+          uint32_t n = 0;
 #pragma unroll
-      for (int t = 0; t < C::TURNS; ++t) {
-        if (t == last_turn || (t - nq % C::TURNS + C::TURNS) % C::TURNS >= tiles) continue;  // no sum to send
-        float* slot = sums + ((n_sent[t] & 1) * C::TURNS + t) * (MT * 128) + 32 * kw + lane;
-        if (turn == t) {  // the slot's last sum has been collected
-          ok = __all_sync(0xffffffffu, count_wait_bounded(&collected[t * 4 * MT + kw], n_sent[t] < 2 ? 0 : n_sent[t] - 1,
-                                                          abort_flag, &timed_out));
+          for (int t = 0; t < C::TURNS; ++t)
+            if (t == last_turn) n = n_sent[t]++;
+          const int ch = channel(turn, last_turn);
+          // the slot's last sum has been collected
+          ok = __all_sync(0xffffffffu, count_wait_bounded(&collected[ch], n < 2 ? 0 : n - 1, abort_flag, &timed_out));
           if (!ok) break;
-          *slot = w;
+          sums[((n & 1) * (C::TURNS * C::TURNS * 4 * MT) + ch) * 32 + lane] = w;
           __syncwarp();
-          if (lane == 0) red_release_add(&sent[t * 4 * MT + kw], 1);
-        } else if (turn == last_turn) {
-          ok = __all_sync(0xffffffffu, count_wait_bounded(&sent[t * 4 * MT + kw], n_sent[t] + 1, abort_flag, &timed_out));
-          if (!ok) break;
-          w += *slot;
-          __syncwarp();
-          if (lane == 0) red_release_add(&collected[t * 4 * MT + kw], 1);
+          if (lane == 0) red_release_add(&sent[ch], 1);
         }
-        ++n_sent[t];
+      } else {
+#pragma unroll
+        for (int t = 0; t < C::TURNS; ++t) {
+          if (t == last_turn || (t - nq % C::TURNS + C::TURNS) % C::TURNS >= tiles) continue;  // no sum from there
+          const uint32_t n = n_got[t]++;
+          const int ch = channel(t, turn);
+          ok = ok && __all_sync(0xffffffffu, count_wait_bounded(&sent[ch], n + 1, abort_flag, &timed_out));
+          if (!ok) break;
+          w += sums[((n & 1) * (C::TURNS * C::TURNS * 4 * MT) + ch) * 32 + lane];
+          __syncwarp();
+          if (lane == 0) red_release_add(&collected[ch], 1);
+        }
       }
       nq += tiles;
       if (!ok || turn != last_turn) continue;
-      if (key < p.n_kv) {
-        const size_t at = (size_t)g.bkv * p.n_acc + key;
-        p.acc_out[at] = (p.acc ? p.acc[at] : 0.f) + w;
-      }
+      if (key < p.n_kv) p.acc_out[at] = before + w;
     }
   }
 
