@@ -270,7 +270,7 @@ namespace {
 // Units of 256 keys where every unit has at least eight query tiles to stream past them and there is a unit
 // for every SM; else of 128.
 bool prompt_wide(const sdpa::PromptWeightsParams& p, int) {
-  return (long long)p.group * ((p.n_q + 127) / 128) >= 8 && (long long)p.bkv * ((p.n_kv + 255) / 256) >= 148;
+  return (long long)p.bkv * ((p.n_kv + 255) / 256) >= 148;
 }
 
 template <int D, int MT>

@@ -36,7 +36,7 @@ struct PromptWeightsParams {
 };
 
 #ifndef SDPA_PROMPT_POLY_EVERY
-#define SDPA_PROMPT_POLY_EVERY 4
+#define SDPA_PROMPT_POLY_EVERY 8
 #endif
 #ifndef SDPA_PROMPT_GROUPS
 #define SDPA_PROMPT_GROUPS 4
@@ -46,8 +46,8 @@ template <int D, int MT>
 struct PromptCfg {
   static constexpr int TILE_BYTES = 128 * D * 2;
   static constexpr int BLOCK_BYTES = 128 * 64 * 2;  // one 64-channel swizzle block
-  static constexpr int KSLOT = D == 128 ? (MT == 2 ? 1 : 3) : (MT == 2 ? 3 : 6);
-  static constexpr int QSLOT = D == 128 ? (MT == 2 ? 4 : 3) : (MT == 2 ? 6 : 6);
+  static constexpr int KSLOT = D == 128 ? (MT == 2 ? 2 : 3) : (MT == 2 ? 4 : 6);
+  static constexpr int QSLOT = D == 128 ? (MT == 2 ? 2 : 3) : (MT == 2 ? 4 : 6);
   static constexpr int NSTAGE = 512 / (128 * MT);
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KSLOT * MT * TILE_BYTES;
@@ -177,27 +177,42 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
 
   // Units: key unit by key unit, the (sequence, key/value head) slices side by side; under a causal mask the first
   // keys have the most queries, so the heaviest come first, and successive rounds are dealt in alternating directions.
-  const int n_units = p.bkv * p.n_kt;
-  auto unit_of = [&](int k) {
-    const int G = (int)gridDim.x, b = (int)blockIdx.x;
-    return (k & 1) ? (k + 1) * G - 1 - b : k * G + b;
-  };
-  const int off = p.n_kv - p.n_q;
-  const int n_qt = (p.n_q + 127) / 128;
+  // (Round k of CTA b, of G: unit k G + b, or (k + 1) G - 1 - b where k is odd.  A walk steps from one to the next without
+  // a division: with one query tile a unit, the roles' own arithmetic is what a unit costs.)
+  const int n_units = p.bkv * p.n_kt, off = p.n_kv - p.n_q, n_qt = (p.n_q + 127) / 128;
+  const int step_even = 2 * ((int)gridDim.x - 1 - (int)blockIdx.x) + 1, step_odd = 2 * (int)blockIdx.x + 1;
+  const int even_q = step_even / p.bkv, even_r = step_even % p.bkv, odd_q = step_odd / p.bkv, odd_r = step_odd % p.bkv;
   struct Unit {
-    int bkv, key0, qt0;  // first key; query tiles [qt0, n_qt) of every head of the group
+    int u, k;       // number, round
+    int kt, bkv;    // u / p.bkv, u % p.bkv
+    int key0, qt0;  // first key; query tiles [qt0, n_qt) of every head of the group
   };
-  auto unit_at = [&](int u) {
-    Unit g;
-    g.bkv = u % p.bkv;
-    g.key0 = (u / p.bkv) * 128 * MT;
+  auto place = [&](Unit& g) {
+    g.key0 = g.kt * (128 * MT);
     const int first = p.causal ? g.key0 - off : 0;  // the first query that sees the unit's first key
     g.qt0 = first > 0 ? first / 128 : 0;
-    return g;
+    return g.u < n_units;
   };
-  auto q_head = [&](int bkv, int h) {  // row of [B Hq]
-    return (bkv / p.heads_kv) * p.heads_q + (bkv % p.heads_kv) * p.group + h;
+  auto begin = [&](Unit& g) {
+    g.u = (int)blockIdx.x;
+    g.k = 0;
+    g.kt = g.u / p.bkv;
+    g.bkv = g.u % p.bkv;
+    return place(g);
   };
+  auto advance = [&](Unit& g) {
+    const bool odd = g.k & 1;
+    g.u += odd ? step_odd : step_even;
+    g.kt += odd ? odd_q : even_q;
+    g.bkv += odd ? odd_r : even_r;
+    if (g.bkv >= p.bkv) {
+      g.bkv -= p.bkv;
+      ++g.kt;
+    }
+    ++g.k;
+    return place(g);
+  };
+  auto q_head = [&](int bkv, int h) { return bkv * p.group + h; };  // row of [B Hq]
 
   if (tmem_bad) {
   } else if (warp == 0) {
@@ -207,8 +222,8 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       tma_prefetch_desc(&tmK);
       int nk = 0, nq = 0;  // units and query tiles loaded
       bool ok = true;
-      for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
-        const Unit g = unit_at(u);
+      Unit g;
+      for (bool more = begin(g); ok && more; more = advance(g)) {
         if (g.qt0 >= n_qt) continue;
         const int ks = nk % C::KSLOT;
         if (!(ok = mbar_wait_bounded(&k_empty[ks], ((uint32_t)(nk / C::KSLOT) & 1u) ^ 1u, abort_flag, &timed_out))) break;
@@ -245,8 +260,8 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024), dQ = smem_desc_sw128(smem_u32(sQ), 16, 1024);
       int nk = 0, nq = 0;
       bool ok = true;
-      for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
-        const Unit g = unit_at(u);
+      Unit g;
+      for (bool more = begin(g); ok && more; more = advance(g)) {
         if (g.qt0 >= n_qt) continue;
         const int ks = nk % C::KSLOT;
         if (!(ok = mbar_wait_bounded(&k_full[ks], (uint32_t)(nk / C::KSLOT) & 1u, abort_flag, &timed_out))) break;
@@ -282,30 +297,22 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
     // ------------------------------------------------------------------ log-sum-exps, negated, base 2
     // Two warps take turns; each has its next tile's values on the way while it waits for a stage.
     struct Walk {  // over the query tiles of this CTA
-      int k, h, qt;
+      int h, qt;
       Unit g;
     };
-    auto settle = [&](Walk& x) {  // on to a tile that exists; false: none is left
-      for (;;) {
-        const int u = unit_of(x.k);
-        if (u >= n_units) return false;
-        if (x.qt < 0) {
-          x.g = unit_at(u);
-          x.qt = x.g.qt0;
-          x.h = 0;
-        }
-        if (x.qt >= n_qt && x.g.qt0 < n_qt) {
-          x.qt = x.g.qt0;
-          ++x.h;
-        }
-        if (x.qt < n_qt && x.h < p.group) return true;
-        ++x.k;
-        x.qt = -1;
-      }
+    auto settle = [&](Walk& x, bool more) {  // on to a unit with tiles; false: none is left
+      while (more && x.g.qt0 >= n_qt) more = advance(x.g);
+      x.h = 0;
+      x.qt = x.g.qt0;
+      return more;
     };
     auto next = [&](Walk& x) {
-      ++x.qt;
-      return settle(x);
+      if (++x.qt < n_qt) return true;
+      if (++x.h < p.group) {
+        x.qt = x.g.qt0;
+        return true;
+      }
+      return settle(x, advance(x.g));
     };
     auto fetch = [&](const Walk& x, float (&v)[4]) {
       const float* L = p.LSE + (size_t)q_head(x.g.bkv, x.h) * p.n_q;
@@ -316,8 +323,9 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       }
     };
     int x_rows = 0, next_rows = 0;  // rows of the tile that exist
-    Walk x = {0, 0, -1, {}};
-    bool more = settle(x);
+    Walk x;
+    bool more = begin(x.g);
+    more = settle(x, more);
     if (more && warp == 3) more = next(x);
     float v[4];
     if (more) fetch(x, v), x_rows = p.n_q - 128 * x.qt;
@@ -355,8 +363,8 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
     int nq = 0;             // query tiles of the units so far
     uint32_t n_sent[C::TURNS] = {}, n_got[C::TURNS] = {};  // sums sent to and collected from each turn
     bool ok = true;
-    for (int k = 0, u; ok && (u = unit_of(k)) < n_units; ++k) {
-      const Unit g = unit_at(u);
+    Unit g;
+    for (bool more = begin(g); ok && more; more = advance(g)) {
       const int tiles_head = n_qt - g.qt0 > 0 ? n_qt - g.qt0 : 0, tiles = p.group * tiles_head;
       const int key = g.key0 + 32 * kw + lane;
       const int warp_last = g.key0 + 32 * kw + 31;  // the warp's last key: masks the most
