@@ -81,6 +81,8 @@ extern "C" int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens,
   p.H = heads;
   p.n_rows = n_rows;
   p.n_cap = n_kv_cap;
+  p.by_rows = sdpa::FastDiv::of((uint32_t)n_rows);
+  p.by_heads = sdpa::FastDiv::of((uint32_t)heads);
   return launch_kv4_rows<false>(p, d, (cudaStream_t)stream);
 }
 
@@ -106,6 +108,8 @@ extern "C" int sdpa_kv4_load(const void* k_codes, const void* k_scales, const vo
   p.H = heads;
   p.n_rows = n_rows;
   p.n_cap = n_kv_cap;
+  p.by_rows = sdpa::FastDiv::of((uint32_t)n_rows);
+  p.by_heads = sdpa::FastDiv::of((uint32_t)heads);
   return launch_kv4_rows<true>(p, d, (cudaStream_t)stream);
 }
 

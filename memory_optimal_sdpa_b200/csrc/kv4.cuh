@@ -11,6 +11,9 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "decode.cuh"
 #include "sm100.cuh"
@@ -22,6 +25,20 @@ struct Kv4Cache {
   uint32_t* scales; // [B, H, n_cap, NG] (s in bits 0 .. 15, m in bits 16 .. 31)
 };
 
+// Unsigned division by a number fixed at launch, for dividends below 2^31 (multiply high, then shift).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  static FastDiv of(uint32_t d) {
+    FastDiv f = {d, 0, 0};
+    while ((1ull << f.shift) < d) ++f.shift;  // 2^(shift - 1) < d <= 2^shift
+    f.mul = (uint32_t)(((1ull << (31 + f.shift)) + d - 1) / d);  // ceil: exact for dividends below 2^31
+    return f;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((unsigned long long)n * mul) >> (31 + shift));
+  }
+};
+
 struct Kv4RowsParams {
   Kv4Cache cache[2];          // K, V
   __nv_bfloat16* rows[2];     // [B, H, n_rows, D]
@@ -29,6 +46,7 @@ struct Kv4RowsParams {
   const int* kv_lens;         // [B]
   const int* n_new;           // append: [B] or null
   int B, H, n_rows, n_cap;
+  FastDiv by_rows, by_heads;
 };
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t bits) { return __uint_as_float(bits << 16); }
@@ -47,63 +65,80 @@ __device__ __forceinline__ uint32_t kv4_scale_bits(float lo, float hi) {
   return s;
 }
 
-// round((x - lo) / s), halves to even, of the exact quotient; inv ~ 1 / s.  The estimate t is within 1e-5 of
-// the quotient; within that distance of a half the sign of x - lo - (k + 1/2) s decides, which the two-sum
-// x - lo = a + e and a fused multiply-add give exactly.
-__device__ __forceinline__ uint32_t kv4_code(float x, float lo, float s, float inv) {
-  const float a = x - lo;
-  const float t = a * inv;
-  float k = rintf(t);
+// round((x - lo) / s), halves to even, of the exact quotient, where the estimate t of the quotient is too near a half
+// to tell: the sign of x - lo - (k + 1/2) s decides, which the two-sum x - lo = a + e and a fused multiply-add give exactly.
+__device__ __noinline__ float kv4_code_exact(float x, float lo, float s, float t) {
   const float half = floorf(t) + 0.5f;
-  if (fabsf(t - half) < 2e-5f) {
-    const float z = a - x;
-    const float e = (x - (a - z)) - (lo + z);
-    const float r = fmaf(-half, s, a);
-    const float below = half - 0.5f;
-    const bool up = r > -e || (r == -e && ((int)below & 1));
-    k = up ? below + 1.f : below;
-  }
-  return (uint32_t)(int)k;
+  if (fabsf(t - half) >= 2e-5f) return rintf(t);
+  const float a = x - lo;
+  const float z = a - x;
+  const float e = (x - (a - z)) - (lo + z);
+  const float r = fmaf(-half, s, a);
+  const float below = half - 0.5f;
+  return r > -e || (r == -e && ((int)below & 1)) ? below + 1.f : below;
 }
 
-// The eight codes of this thread's channels, and the group's scale and minimum (bits).  The four threads of
-// a group are lanes differing in bits 0 and 1.
-__device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scale_bits, uint32_t& min_bits) {
-  float x[8];
-  bf16x8_to_f32(raw, x);
-  float lo = x[0], hi = x[0], bad = 0.f;
+// Smaller and larger of two pairs of bf16, NaN if either is.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The codes of this thread's eight channels (as floats and packed), and the group's scale (bits 0 .. 15) and minimum.
+// The four threads of a group are lanes differing in bits 0 and 1.
+__device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scale, float (&code)[8]) {
+  const uint32_t mn = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
+  const uint32_t mx = max_bf16x2(max_bf16x2(raw.x, raw.y), max_bf16x2(raw.z, raw.w));
+  // the smallest and minus the largest of the eight, then of the group
+  uint32_t both = min_bf16x2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+  both = (both & 0xFFFFu) | ((max_bf16x2(mx, mx >> 16) << 16) ^ 0x80000000u);
+  both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+  both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+  float lo = __uint_as_float(both << 16), hi = -__uint_as_float(both & 0xFFFF0000u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad += x[i] * 0.f;  // NaN for a NaN or an infinity
-  }
-#pragma unroll
-  for (int off = 1; off <= 2; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-    bad += __shfl_xor_sync(0xffffffffu, bad, off);
-  }
-  if (bad != 0.f) {  // NaN: the four threads agree
-    scale_bits = min_bits = 0x7FC0u;
+  for (int i = 0; i < 8; ++i) code[i] = 0.f;
+  if (!(lo >= -FLT_MAX && hi <= FLT_MAX)) {  // a NaN or an infinity
+    scale = 0x7FC07FC0u;
+    code[0] = code[1] = code[2] = code[3] = code[4] = code[5] = code[6] = code[7] = 0.f;
     return 0u;
   }
   // Differences of values near the largest float would overflow: work 2^-16 smaller there.
   const float big = fmaxf(fabsf(lo), fabsf(hi));
   const float down = big > 0x1p120f ? 0x1p-16f : 1.f;
-  min_bits = __float_as_uint(lo) >> 16;
   const float s_down = bf16_bits_to_float(kv4_scale_bits(lo * down, hi * down));
-  scale_bits = __float_as_uint(s_down / down) >> 16;
+  const uint32_t scale_bits = __float_as_uint(s_down / down) >> 16;
+  scale = scale_bits | (both << 16);
   if (s_down == 0.f) return 0u;
   // and the reciprocal of a tiny scale would: work 2^64 larger there (both factors are exact)
   const float f = big < 0x1p-60f ? 0x1p64f : down;
   const float s = bf16_bits_to_float(scale_bits) * f;
   lo *= f;
-  const float inv = 1.f / s;
-  uint32_t codes = 0;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  float x[8], t[8], far = 0.f;
+  bf16x8_to_f32(raw, x);
+  constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to a whole number, halves to even
 #pragma unroll
-  for (int i = 0; i < 8; ++i) codes |= kv4_code(x[i] * f, lo, s, inv) << (4 * i);
-  return codes;
+  for (int i = 0; i < 8; ++i) {
+    x[i] *= f;
+    t[i] = (x[i] - lo) * inv;  // within 1e-5 of the quotient
+    code[i] = (t[i] + ROUND) - ROUND;
+    far = fmaxf(far, fabsf(t[i] - code[i]));
+  }
+  if (far > 0.49998f) {  // one of them is near a half
+#pragma unroll
+    for (int i = 0; i < 8; ++i) code[i] = kv4_code_exact(x[i], lo, s, t[i]);
+  }
+  // 16-bit pieces as whole numbers in fp32, read off the sum with 2^23
+  const float p0 = fmaf(code[3], 4096.f, fmaf(code[2], 256.f, fmaf(code[1], 16.f, code[0] + 8388608.f)));
+  const float p1 = fmaf(code[7], 4096.f, fmaf(code[6], 256.f, fmaf(code[5], 16.f, code[4] + 8388608.f)));
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x5410);
 }
 
 // A thread's eight codes are the 16-bit pieces r = 2 t (low half) and 2 t + 1 (high half) of its group; the
@@ -126,14 +161,22 @@ __device__ __forceinline__ uint32_t kv4_from_words(uint32_t word, int lane) {
 }
 
 // s c + m for eight codes, rounded to bf16 (s c is exact in fp32).
-__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t scale) {
+__device__ __forceinline__ uint4 kv4_values(const float (&code)[8], uint32_t scale) {
   const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xFFFF0000u);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = sm100::pack_bf16x2(fmaf(s, (float)((codes >> (8 * i)) & 15u), m),
-                              fmaf(s, (float)((codes >> (8 * i + 4)) & 15u), m));
+  for (int i = 0; i < 4; ++i) w[i] = sm100::pack_bf16x2(fmaf(s, code[2 * i], m), fmaf(s, code[2 * i + 1], m));
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Eight packed codes as floats: two at a time as fp16 1024 + c, which is exact.
+__device__ __forceinline__ void kv4_unpack(uint32_t codes, float (&code)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // channels i and 4 + i
+    const uint32_t h = ((codes >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
+    const float2 v = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1024.f)));
+    code[i] = v.x;
+    code[4 + i] = v.y;
+  }
 }
 
 constexpr int KV4_THREADS = 256;
@@ -154,8 +197,10 @@ __global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4Row
   constexpr int RPB = KV4_THREADS / TPR;   // rows per block and pass
   const int lane = threadIdx.x & 31;
   const int part = threadIdx.x % TPR, g = part >> 2, t = part & 3;
-  const Kv4Cache c = p.cache[blockIdx.y];
-  __nv_bfloat16* rows = p.rows[blockIdx.y];
+  const bool second = blockIdx.y != 0;
+  const Kv4Cache c = {second ? p.cache[1].codes : p.cache[0].codes, second ? p.cache[1].scales : p.cache[0].scales};
+  __nv_bfloat16* rows = second ? p.rows[1] : p.rows[0];
+  __nv_bfloat16* read = second ? p.read[1] : p.read[0];
   const uint32_t total = (uint32_t)p.B * p.H * p.n_rows;
   const uint32_t first = blockIdx.x * (uint32_t)(RPB * KV4_UNROLL) + threadIdx.x / TPR;
   bool on[KV4_UNROLL];
@@ -165,7 +210,7 @@ __global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4Row
     const uint32_t slot = first + u * RPB;
     on[u] = false;
     if (slot < total) {
-      const uint32_t bh = slot / (uint32_t)p.n_rows, row = slot - bh * p.n_rows, b = bh / (uint32_t)p.H;
+      const uint32_t bh = p.by_rows.div(slot), row = slot - bh * p.n_rows, b = p.by_heads.div(bh);
       const int len = cache_len(p.kv_lens, b, p.n_cap);
       int to = (int)row;
       if (LOAD) {
@@ -189,7 +234,9 @@ __global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4Row
     }
 #pragma unroll
     for (int u = 0; u < KV4_UNROLL; ++u) {
-      const uint4 v = kv4_values(kv4_from_words<NG>(word[u], lane), scale[u]);
+      float code[8];
+      kv4_unpack(kv4_from_words<NG>(word[u], lane), code);
+      const uint4 v = kv4_values(code, scale[u]);
       if (on[u]) *reinterpret_cast<uint4*>(rows + at[u]) = v;
     }
   } else {
@@ -198,14 +245,13 @@ __global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4Row
     for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = on[u] ? ld_nc_v4(rows + at[u]) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < KV4_UNROLL; ++u) {
-      uint32_t s, m;
-      const uint32_t codes = kv4_quantise(raw[u], s, m);
-      const uint32_t word = kv4_to_words<NG>(codes, lane);
+      uint32_t scale;
+      float code[8];
+      const uint32_t word = kv4_to_words<NG>(kv4_quantise(raw[u], scale, code), lane);
       if (on[u]) {
         *reinterpret_cast<uint32_t*>(c.codes + cache_row[u] * (D / 2) + 4 * (t * NG + g)) = word;
-        if (t == 0) c.scales[cache_row[u] * NG + g] = s | (m << 16);
-        if (p.read[blockIdx.y])
-          *reinterpret_cast<uint4*>(p.read[blockIdx.y] + at[u]) = kv4_values(codes, s | (m << 16));
+        if (t == 0) c.scales[cache_row[u] * NG + g] = scale;
+        if (read) *reinterpret_cast<uint4*>(read + at[u]) = kv4_values(code, scale);
       }
     }
   }
