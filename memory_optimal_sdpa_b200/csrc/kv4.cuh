@@ -65,17 +65,17 @@ __device__ __forceinline__ uint32_t kv4_scale_bits(float lo, float hi) {
   return s;
 }
 
-// round((x - lo) / s), halves to even, of the exact quotient, where the estimate t of the quotient is too near a half
-// to tell: the sign of x - lo - (k + 1/2) s decides, which the two-sum x - lo = a + e and a fused multiply-add give exactly.
-__device__ __noinline__ float kv4_code_exact(float x, float lo, float s, float t) {
-  const float half = floorf(t) + 0.5f;
-  if (fabsf(t - half) >= 2e-5f) return rintf(t);
+// (x - lo) / s rounded to a whole number, halves to even, by the exact quotient, where its estimate is too near a half
+// to tell; code: the estimate rounded.  x - lo = a + e exactly (two-sum), d = a - code s is exact (fused, and no
+// more bits than a), and so is |d| - s / 2 next to a half; then e decides, and the code's parity where all is equal.
+__device__ __forceinline__ float kv4_code_exact(float x, float lo, float s, float code) {
   const float a = x - lo;
   const float z = a - x;
   const float e = (x - (a - z)) - (lo + z);
-  const float r = fmaf(-half, s, a);
-  const float below = half - 0.5f;
-  return r > -e || (r == -e && ((int)below & 1)) ? below + 1.f : below;
+  const float d = fmaf(-code, s, a);
+  const float one = copysignf(1.f, d);
+  const float over = fmaf(-0.5f, s, fabsf(d)), rest = -one * e;  // past the half by over - rest
+  return over > rest || (over == rest && ((int)code & 1)) ? code + one : code;
 }
 
 // Smaller and larger of two pairs of bf16, NaN if either is.
@@ -112,7 +112,7 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scal
   const float big = fmaxf(fabsf(lo), fabsf(hi));
   const float down = big > 0x1p120f ? 0x1p-16f : 1.f;
   const float s_down = bf16_bits_to_float(kv4_scale_bits(lo * down, hi * down));
-  const uint32_t scale_bits = __float_as_uint(s_down / down) >> 16;
+  const uint32_t scale_bits = __float_as_uint(s_down * (big > 0x1p120f ? 0x1p16f : 1.f)) >> 16;
   scale = scale_bits | (both << 16);
   if (s_down == 0.f) return 0u;
   // and the reciprocal of a tiny scale would: work 2^64 larger there (both factors are exact)
@@ -123,17 +123,19 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scal
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   float x[8], t[8], far = 0.f;
   bf16x8_to_f32(raw, x);
+  const bool other = f != 1.f;
   constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to a whole number, halves to even
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] *= f;
+    if (other) x[i] *= f;
     t[i] = (x[i] - lo) * inv;  // within 1e-5 of the quotient
     code[i] = (t[i] + ROUND) - ROUND;
     far = fmaxf(far, fabsf(t[i] - code[i]));
   }
   if (far > 0.49998f) {  // one of them is near a half
 #pragma unroll
-    for (int i = 0; i < 8; ++i) code[i] = kv4_code_exact(x[i], lo, s, t[i]);
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(t[i] - code[i]) > 0.49998f) code[i] = kv4_code_exact(x[i], lo, s, code[i]);
   }
   // 16-bit pieces as whole numbers in fp32, read off the sum with 2^23
   const float p0 = fmaf(code[3], 4096.f, fmaf(code[2], 256.f, fmaf(code[1], 16.f, code[0] + 8388608.f)));
@@ -190,70 +192,116 @@ __device__ __forceinline__ int cache_len(const int* kv_lens, int b, int n_cap) {
   return len < 0 ? 0 : n_cap;
 }
 
-// LOAD false: append.  Grid: x blocks over the B H n_rows row slots, y: K, V.
-template <int D, bool LOAD>
-__global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4RowsParams p) {
-  constexpr int NG = D / 32, TPR = D / 8;  // threads per row
-  constexpr int RPB = KV4_THREADS / TPR;   // rows per block and pass
-  const int lane = threadIdx.x & 31;
-  const int part = threadIdx.x % TPR, g = part >> 2, t = part & 3;
-  const bool second = blockIdx.y != 0;
-  const Kv4Cache c = {second ? p.cache[1].codes : p.cache[0].codes, second ? p.cache[1].scales : p.cache[0].scales};
-  __nv_bfloat16* rows = second ? p.rows[1] : p.rows[0];
-  __nv_bfloat16* read = second ? p.read[1] : p.read[0];
-  const uint32_t total = (uint32_t)p.B * p.H * p.n_rows;
-  const uint32_t first = blockIdx.x * (uint32_t)(RPB * KV4_UNROLL) + threadIdx.x / TPR;
-  bool on[KV4_UNROLL];
-  size_t at[KV4_UNROLL], cache_row[KV4_UNROLL];
-#pragma unroll
-  for (int u = 0; u < KV4_UNROLL; ++u) {
-    const uint32_t slot = first + u * RPB;
-    on[u] = false;
-    if (slot < total) {
-      const uint32_t bh = p.by_rows.div(slot), row = slot - bh * p.n_rows, b = p.by_heads.div(bh);
-      const int len = cache_len(p.kv_lens, b, p.n_cap);
-      int to = (int)row;
-      if (LOAD) {
-        on[u] = to < len;
-      } else {
-        const int n = p.n_new ? p.n_new[b] : p.n_rows;
-        if (n < 0 || n > p.n_rows || n > p.n_cap - len) record_error(7 /* SDPA_ERR_DEVICE_BAD_LENGTH */);
-        on[u] = to < n && to < p.n_cap - len;
-        to += len;
-      }
-      at[u] = (size_t)slot * D + 8 * part;
-      cache_row[u] = (size_t)bh * p.n_cap + to;
-    }
-  }
+// What a thread moves: KV4_UNROLL rows' parts, each at its own place.
+template <int NG, bool LOAD, class Place>
+__device__ __forceinline__ void kv4_move(const Place& place, bool want_read, int lane, bool first_of_group) {
   if (LOAD) {
     uint32_t word[KV4_UNROLL], scale[KV4_UNROLL];
 #pragma unroll
     for (int u = 0; u < KV4_UNROLL; ++u) {
-      word[u] = on[u] ? *reinterpret_cast<const uint32_t*>(c.codes + cache_row[u] * (D / 2) + 4 * (t * NG + g)) : 0u;
-      scale[u] = on[u] ? c.scales[cache_row[u] * NG + g] : 0u;
+      word[u] = place.on(u) ? *place.codes(u) : 0u;
+      scale[u] = place.on(u) ? *place.scales(u) : 0u;
     }
 #pragma unroll
     for (int u = 0; u < KV4_UNROLL; ++u) {
       float code[8];
       kv4_unpack(kv4_from_words<NG>(word[u], lane), code);
-      const uint4 v = kv4_values(code, scale[u]);
-      if (on[u]) *reinterpret_cast<uint4*>(rows + at[u]) = v;
+      if (place.on(u)) *place.row(u) = kv4_values(code, scale[u]);
     }
   } else {
     uint4 raw[KV4_UNROLL];
 #pragma unroll
-    for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = on[u] ? ld_nc_v4(rows + at[u]) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = place.on(u) ? ld_nc_v4(place.row(u)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < KV4_UNROLL; ++u) {
       uint32_t scale;
       float code[8];
       const uint32_t word = kv4_to_words<NG>(kv4_quantise(raw[u], scale, code), lane);
-      if (on[u]) {
-        *reinterpret_cast<uint32_t*>(c.codes + cache_row[u] * (D / 2) + 4 * (t * NG + g)) = word;
-        if (t == 0) c.scales[cache_row[u] * NG + g] = scale;
-        if (read) *reinterpret_cast<uint4*>(read + at[u]) = kv4_values(code, scale);
+      if (place.on(u)) {
+        *place.codes(u) = word;
+        if (first_of_group) *place.scales(u) = scale;
+        if (want_read) *place.read(u) = kv4_values(code, scale);
       }
     }
+  }
+}
+
+// LOAD false: append.  Grid: x blocks over the B H n_rows row slots, y: K, V.  A block whose rows are all of one
+// sequence and head (every block of a long prompt) knows its places as one base and fixed offsets, and leaves at once where no
+// row is to be moved; the others (single tokens) find each row's place by itself.
+template <int D, bool LOAD>
+__global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4RowsParams p) {
+  constexpr int NG = D / 32, TPR = D / 8;  // threads per row
+  constexpr int RPB = KV4_THREADS / TPR;   // rows per block and pass
+  const int lane = threadIdx.x & 31;
+  const int part = threadIdx.x % TPR, g = part >> 2, t = part & 3, mine = threadIdx.x / TPR;
+  const bool second = blockIdx.y != 0;
+  uint8_t* codes = (second ? p.cache[1].codes : p.cache[0].codes) + 4 * (t * NG + g);
+  uint32_t* scales = (second ? p.cache[1].scales : p.cache[0].scales) + g;
+  __nv_bfloat16* rows = (second ? p.rows[1] : p.rows[0]) + 8 * part;
+  __nv_bfloat16* read = second ? p.read[1] : p.read[0];
+  const bool want_read = read != nullptr;
+  if (want_read) read += 8 * part;
+  const uint32_t total = (uint32_t)p.B * p.H * p.n_rows, first = blockIdx.x * (uint32_t)(RPB * KV4_UNROLL);
+  // Rows of sequence b that are moved, and the cache row of the first.
+  auto limits = [&](uint32_t b, int& limit, int& to) {
+    const int len = cache_len(p.kv_lens, b, p.n_cap);
+    to = LOAD ? 0 : len;
+    limit = len;
+    if (!LOAD) {
+      const int n = p.n_new ? p.n_new[b] : p.n_rows;
+      if (n < 0 || n > p.n_rows || n > p.n_cap - len) record_error(7 /* SDPA_ERR_DEVICE_BAD_LENGTH */);
+      limit = min(n, p.n_cap - len);
+    }
+    limit = min(limit, p.n_rows);
+  };
+  const uint32_t bh0 = p.by_rows.div(first), row0 = first - bh0 * p.n_rows;
+  if (row0 + RPB * KV4_UNROLL <= (uint32_t)p.n_rows) {
+    struct Place {
+      uint8_t *c, *s, *x, *r;
+      int left;  // rows from this thread's first one to the limit
+      __device__ __forceinline__ bool on(int u) const { return u * RPB < left; }
+      __device__ __forceinline__ uint32_t* codes(int u) const { return (uint32_t*)(c + u * (RPB * (D / 2))); }
+      __device__ __forceinline__ uint32_t* scales(int u) const { return (uint32_t*)(s + u * (RPB * NG * 4)); }
+      __device__ __forceinline__ uint4* row(int u) const { return (uint4*)(x + u * (RPB * D * 2)); }
+      __device__ __forceinline__ uint4* read(int u) const { return (uint4*)(r + u * (RPB * D * 2)); }
+    };
+    int limit, to;
+    limits(p.by_heads.div(bh0), limit, to);
+    if ((int)row0 >= limit) return;
+    const int row = (int)row0 + mine;
+    const size_t cache_row = (size_t)bh0 * p.n_cap + to + row, at = (size_t)(first + mine) * D;
+    const Place place = {codes + cache_row * (D / 2), (uint8_t*)(scales + cache_row * NG), (uint8_t*)(rows + at),
+                         (uint8_t*)(want_read ? read + at : nullptr), limit - row};
+    kv4_move<NG, LOAD>(place, want_read, lane, t == 0);
+  } else {
+    struct Place {
+      uint32_t *c[KV4_UNROLL], *s[KV4_UNROLL];
+      uint4 *x[KV4_UNROLL], *r[KV4_UNROLL];
+      bool o[KV4_UNROLL];
+      __device__ __forceinline__ bool on(int u) const { return o[u]; }
+      __device__ __forceinline__ uint32_t* codes(int u) const { return c[u]; }
+      __device__ __forceinline__ uint32_t* scales(int u) const { return s[u]; }
+      __device__ __forceinline__ uint4* row(int u) const { return x[u]; }
+      __device__ __forceinline__ uint4* read(int u) const { return r[u]; }
+    } place;
+#pragma unroll
+    for (int u = 0; u < KV4_UNROLL; ++u) {
+      const uint32_t slot = first + mine + u * RPB;
+      place.o[u] = false;
+      if (slot < total) {
+        const uint32_t bh = p.by_rows.div(slot), row = slot - bh * p.n_rows;
+        int limit, to;
+        limits(p.by_heads.div(bh), limit, to);
+        place.o[u] = (int)row < limit;
+        const size_t cache_row = (size_t)bh * p.n_cap + to + row, at = (size_t)slot * D;
+        place.c[u] = (uint32_t*)(codes + cache_row * (D / 2));
+        place.s[u] = scales + cache_row * NG;
+        place.x[u] = (uint4*)(rows + at);
+        if (want_read) place.r[u] = (uint4*)(read + at);
+      }
+    }
+    kv4_move<NG, LOAD>(place, want_read, lane, t == 0);
   }
 }
 
