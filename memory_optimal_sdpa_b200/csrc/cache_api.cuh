@@ -369,22 +369,45 @@ int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens,
   if (int e = check_device()) return e;
   cudaStream_t s = (cudaStream_t)stream;
   sdpa::EvictParams p = {acc, acc_out, kv_lens, keep, new_lens, heads, n_cap, n_out, budget, recent};
-  sdpa::sdpa_evict_select_kernel<<<(unsigned)bh, sdpa::EVICT_THREADS, 0, s>>>(p);
-  sdpa::EvictRowsParams r = {};
-  for (int i = 0; i < n; ++i) {
-    r.src[i] = (const uint8_t*)arrays[i].in;
-    r.dst[i] = (uint8_t*)arrays[i].out;
-    r.row_bytes[i] = (int)arrays[i].row_bytes;
+  if (n_cap <= sdpa::EVICT_CACHED) {
+    static std::atomic<uint64_t> ready{0};
+    if (int e = allow_smem(sdpa::sdpa_evict_select_kernel<true>, sdpa::EVICT_CACHED * 4, ready)) return e;
+    sdpa::sdpa_evict_select_kernel<true><<<(unsigned)bh, sdpa::EVICT_THREADS, (size_t)n_cap * 4, s>>>(p);
+  } else {
+    sdpa::sdpa_evict_select_kernel<false><<<(unsigned)bh, sdpa::EVICT_THREADS, 0, s>>>(p);
   }
-  r.keep = keep;
-  r.kv_lens = kv_lens;
-  r.n_arrays = n;
-  r.H = heads;
-  r.n_cap = n_cap;
-  r.n_out = n_out;
-  r.budget = budget;
-  sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)bh, (unsigned)n), 256, 0, s>>>(r);
-  return launched("evict launch");
+  if (int e = launched("evict select launch")) return e;
+  // Arrays in place and arrays that go elsewhere (a caller may mix them).
+  for (int in_place = 0; in_place < 2; ++in_place) {
+    sdpa::EvictRowsParams r = {};
+    int k = 0;
+    size_t largest = 0;
+    for (int i = 0; i < n; ++i) {
+      if ((arrays[i].in == arrays[i].out) != (in_place == 1)) continue;
+      r.src[k] = (const uint8_t*)arrays[i].in;
+      r.dst[k] = (uint8_t*)arrays[i].out;
+      r.row_bytes[k++] = (int)arrays[i].row_bytes;
+      if (arrays[i].row_bytes > largest) largest = arrays[i].row_bytes;
+    }
+    if (k == 0) continue;
+    r.keep = keep;
+    r.kv_lens = kv_lens;
+    r.H = heads;
+    r.n_cap = n_cap;
+    r.n_out = n_out;
+    r.budget = budget;
+    if (in_place) {
+      const dim3 grid((unsigned)bh, (unsigned)((largest + 63) / 64), (unsigned)k);
+      sdpa::sdpa_evict_rows_in_place_kernel<<<grid, sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
+    } else {
+      const long long per_block = sdpa::EVICT_ROW_THREADS * sdpa::EVICT_ROW_UNROLL * 16 / (long long)largest;
+      long long blocks = (budget + per_block - 1) / per_block;
+      if (blocks > 65535) blocks = 65535;
+      sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)bh, (unsigned)blocks, (unsigned)k), sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
+    }
+    if (int e = launched("evict rows launch")) return e;
+  }
+  return SDPA_OK;
 }
 
 int evict_sizes(int batch, int heads, int n_cap, int n_out, int d, int budget, int recent) {
