@@ -396,14 +396,16 @@ int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens,
     r.n_cap = n_cap;
     r.n_out = n_out;
     r.budget = budget;
+    r.n_bh = (int)bh;
     if (in_place) {
       const dim3 grid((unsigned)bh, (unsigned)((largest + 63) / 64), (unsigned)k);
       sdpa::sdpa_evict_rows_in_place_kernel<<<grid, sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
     } else {
-      const long long per_block = sdpa::EVICT_ROW_THREADS * sdpa::EVICT_ROW_UNROLL * 16 / (long long)largest;
-      long long blocks = (budget + per_block - 1) / per_block;
-      if (blocks > 65535) blocks = 65535;
-      sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)bh, (unsigned)blocks, (unsigned)k), sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
+      // four blocks an SM in all, no more than stretches of the array with the longest rows
+      const long long rows = sdpa::EVICT_ROW_THREADS * sdpa::EVICT_ROW_UNROLL * 16 / (long long)largest;
+      long long blocks = (budget + rows - 1) / rows * (long long)bh;
+      if (blocks > 148 * 4 / k) blocks = 148 * 4 / k;
+      sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)blocks, (unsigned)k), sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
     }
     if (int e = launched("evict rows launch")) return e;
   }
