@@ -23,6 +23,7 @@ The bounded decode cache (C ABI in include/sdpa_cache.h):
 """
 import collections
 import ctypes
+import functools
 import math
 import os
 
@@ -345,21 +346,32 @@ def _fit(t, name, dtype, shape):
     return _tensor(t, name, dtype, shape)
 
 
+def _free(t, name, dtype, ndim):
+    """_tensor for a shape that is free in every entry; returns it."""
+    if getattr(t, "dtype", None) is dtype and t.dim() == ndim and t.is_contiguous():
+        return t.shape
+    return _tensor(t, name, dtype, (None,) * ndim).shape
+
+
 def _kv4(cache, name="cache", B=None, H=None, d=None):
     """Check a Kv4Cache; returns B, H, n_cap, d and its (name, tensor) pairs."""
     import torch
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise TypeError("%s must be a Kv4Cache, got %s" % (name, type(cache).__name__))
     kc, ks, vc, vs = cache
-    _tensor(kc, name + ".k_codes", torch.uint8, (B, H, None, None if d is None else d // 2))
-    codes = kc.shape
+    names = _KV4_NAMES.get(name) or tuple("%s.%s" % (name, x) for x in Kv4Cache._fields)
+    codes = _free(kc, names[0], torch.uint8, 4)
+    if B is not None and (codes[0], codes[1], 2 * codes[3]) != (B, H, d):
+        _tensor(kc, names[0], torch.uint8, (B, H, None, d // 2))
     B, H, n_cap, half = codes
     scales = (B, H, n_cap, half // 16, 2)
-    _fit(ks, name + ".k_scales", torch.bfloat16, scales)
-    _fit(vc, name + ".v_codes", torch.uint8, codes)
-    _fit(vs, name + ".v_scales", torch.bfloat16, scales)
-    return B, H, n_cap, 2 * half, ((name + ".k_codes", kc), (name + ".k_scales", ks), (name + ".v_codes", vc),
-                                   (name + ".v_scales", vs))
+    _fit(ks, names[1], torch.bfloat16, scales)
+    _fit(vc, names[2], torch.uint8, codes)
+    _fit(vs, names[3], torch.bfloat16, scales)
+    return B, H, n_cap, 2 * half, ((names[0], kc), (names[1], ks), (names[2], vc), (names[3], vs))
+
+
+_KV4_NAMES = {name: tuple("%s.%s" % (name, x) for x in Kv4Cache._fields) for name in ("cache", "out")}
 
 
 def _both(name, a, b):
@@ -388,12 +400,14 @@ def _launch(where, dev, stream, *args):
         handle = raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
     else:
         handle = _stream(stream, dev)
+    fn = getattr(lib, where)
     if torch.cuda.current_device() == dev.index:
-        status = getattr(lib, where)(*args, handle)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib, where)(*args, handle)
-    _check(status, where)
+            status = fn(*args, handle)
+    if status != SDPA_OK:
+        _check(status, where)
 
 
 def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, stream=None):
@@ -403,8 +417,8 @@ def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, strea
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     B, H, n_cap, d, parts = _kv4(cache)
-    _tensor(k, "k", bf, (B, H, None, d))
-    rows = k.shape
+    rows = _free(k, "k", bf, 4)
+    _fit(k, "k", bf, (B, H, rows[2], d))
     _fit(v, "v", bf, rows)
     _fit(kv_lens, "kv_lens", i32, (B,))
     if n_new is not None:
@@ -427,8 +441,8 @@ def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
     B, H, n_cap, d, parts = _kv4(cache)
     _both("k and v", k, v)
     if k is not None:
-        _tensor(k, "k", bf, (B, H, n_rows, d))
-        n_rows = k.shape[2]
+        n_rows = _free(k, "k", bf, 4)[2] if n_rows is None else n_rows
+        _fit(k, "k", bf, (B, H, n_rows, d))
         _fit(v, "v", bf, (B, H, n_rows, d))
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
     dev = _device("cache.k_codes", cache[0], *parts[1:], ("kv_lens", kv_lens), ("k", k), ("v", v))
@@ -442,12 +456,13 @@ def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
 
 
 def _acc_args(acc, acc_out, shape):
-    """acc, acc_out of a decode or of fwd_acc: acc_out defaults to acc (the running sum)."""
+    """acc, acc_out of a decode or of fwd_acc (whose last entry is free: None): acc_out defaults to acc (the running sum)."""
     import torch
-    if acc is not None:
-        _tensor(acc, "acc", torch.float32, shape)
-    if acc_out is not None:
-        _tensor(acc_out, "acc_out", torch.float32, shape if acc is None else tuple(acc.shape))
+    for name, t in (("acc", acc), ("acc_out", acc_out)):
+        if t is not None:
+            if shape[2] is None:
+                shape = shape[:2] + tuple(_free(t, name, torch.float32, 3)[2:])
+            _fit(t, name, torch.float32, shape)
     return acc if acc_out is None else acc_out
 
 
@@ -456,8 +471,8 @@ def _decode_run(where, size, q, keys, parts, kv_lens, B, H_kv, n_cap, d, scale, 
     """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size` the workspace's bytes for
     a number of query heads."""
     import torch
-    _tensor(q, "q", torch.bfloat16, (B, None, d))
-    H_q = q.shape[1]
+    H_q = _free(q, "q", torch.bfloat16, 3)[1]
+    _fit(q, "q", torch.bfloat16, (B, H_q, d))
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
     if o is not None:
         _fit(o, "o", torch.bfloat16, q.shape)
@@ -477,6 +492,7 @@ def _decode_run(where, size, q, keys, parts, kv_lens, B, H_kv, n_cap, d, scale, 
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
 def decode_kv4_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc=False):
     return int(lib.sdpa_decode_kv4_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d, int(bool(with_acc))))
 
@@ -494,6 +510,7 @@ def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, a
                        kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d):
     return int(lib.sdpa_decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d))
 
@@ -503,8 +520,7 @@ def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse
     """decode_gqa over a bf16 cache k, v [B,H_kv,n_cap,d] that also sums the keys' attention weights; acc, acc_out (one
     of them at least) and empty slots as in decode_kv4."""
     import torch
-    _tensor(k, "k", torch.bfloat16, (None, None, None, None))
-    B, H_kv, n_cap, d = k.shape
+    B, H_kv, n_cap, d = _free(k, "k", torch.bfloat16, 4)
     _fit(v, "v", torch.bfloat16, k.shape)
     if acc is None and acc_out is None:
         raise ValueError("give acc, acc_out or both")
@@ -521,10 +537,9 @@ def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=
     acc_out = acc + weights for the n_kv keys, in place without acc_out; without both a new [B,H_kv,n_kv] tensor.
     Returns acc_out."""
     import torch
-    _tensor(q, "q", torch.bfloat16, (None, None, None, None))
-    B, H_q, n_q, d = q.shape
-    _tensor(k, "k", torch.bfloat16, (B, None, None, d))
-    H_kv, n_kv = k.shape[1:3]
+    B, H_q, n_q, d = _free(q, "q", torch.bfloat16, 4)
+    _, H_kv, n_kv, _ = _free(k, "k", torch.bfloat16, 4)
+    _fit(k, "k", torch.bfloat16, (B, H_kv, n_kv, d))
     _fit(lse, "lse", torch.float32, (B, H_q, n_q))
     acc_out = _acc_args(acc, acc_out, (B, H_kv, None))
     dev = _device("q", q, ("k", k), ("lse", lse), ("acc", acc), ("acc_out", acc_out))
@@ -565,8 +580,7 @@ def evict(k, v, acc, kv_lens, budget, recent=0, k_out=None, v_out=None, acc_out=
     keep int32 [B,H,budget] (the old rows, -1 past the new length) and the new lengths int32 [B]."""
     import torch
     bf = torch.bfloat16
-    _tensor(k, "k", bf, (None, None, None, None))
-    B, H, n_cap, d = k.shape
+    B, H, n_cap, d = _free(k, "k", bf, 4)
     _fit(v, "v", bf, k.shape)
     _both("k_out and v_out", k_out, v_out)
     n_out, outs, out_parts = n_cap, None, ()
