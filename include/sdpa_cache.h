@@ -47,7 +47,7 @@ extern "C" {
  * s = m = NaN and reads back as NaN.
  * k_read, v_read [batch, heads, n_rows, d] bf16, or both NULL: the values the cache now stands for,
  * s c + m rounded to bf16, for the attention of the rows' own step (rows t >= n_new[b] are left as
- * they were).
+ * they were).  They may not overlap K or V (SDPA_ERR_INVALID_ARG).
  */
 SDPA_API int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens, const int* n_new, void* k_codes,
                              void* k_scales, void* v_codes, void* v_scales, void* k_read, void* v_read, int batch,

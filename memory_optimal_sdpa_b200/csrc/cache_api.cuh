@@ -49,6 +49,10 @@ int allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& ready) {
   return SDPA_OK;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
 bool cache_arrays_aligned(const void* kc, const void* ks, const void* vc, const void* vs) {
   return aligned16(kc) && aligned16(ks) && aligned16(vc) && aligned16(vs);
 }
@@ -67,6 +71,9 @@ extern "C" int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens,
       !aligned16(k_read) || !aligned16(v_read) || !aligned4(kv_lens) || !aligned4(n_new))
     return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads, n_rows) || !cache_sizes_fit(batch, heads, n_kv_cap)) return SDPA_ERR_UNSUPPORTED;
+  const size_t bytes = (size_t)batch * heads * n_rows * d * 2;
+  for (const void* read : {k_read, v_read})  // the inputs are read through the non-coherent path
+    if (read && (overlap(read, bytes, K, bytes) || overlap(read, bytes, V, bytes))) return SDPA_ERR_INVALID_ARG;
   if (int e = check_device()) return e;
   sdpa::Kv4RowsParams p = {};
   p.cache[0] = {(uint8_t*)k_codes, (uint32_t*)k_scales};
@@ -337,10 +344,6 @@ struct EvictArray {
   void* out;
   size_t row_bytes;
 };
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
-}
 
 // arrays[0 .. n) are the cache's rows; the weights are added here.
 int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens, float* acc_out, int* keep,

@@ -67,14 +67,14 @@ struct PromptCfg {
   static constexpr int THREADS = 128 + 128 * GROUPS;
 };
 
-// 2^x for a pair on the FMA pipe, -inf <= x <= 64: as sm100::exp2_poly2 (x = j + f, 2^f by a polynomial, j into the
+// 2^x for a pair on the FMA pipe, x not NaN: as sm100::exp2_poly2 (x = j + f, 2^f by a polynomial, j into the
 // exponent), with a degree-5 polynomial (Remez exchange on [-1/2, 1/2]: relative error 7.5e-8, in fp32 2.1e-7, as
-// ex2.approx has): these weights are results, not rounded to bf16 afterwards.  Below 2^-125 it gives about 2^-125.
+// ex2.approx has): these weights are results, not rounded to bf16 afterwards.  Held between 2^-125 and 2^127.
 __device__ __forceinline__ float2 exp2_fine2(float2 x) {
   using namespace sm100;
   constexpr float SHIFT = 12582912.0f;  // 1.5 * 2^23
-  x.x = fmaxf(x.x, -125.f);
-  x.y = fmaxf(x.y, -125.f);
+  x.x = fminf(fmaxf(x.x, -125.f), 127.f);
+  x.y = fminf(fmaxf(x.y, -125.f), 127.f);
   const float2 t = fadd2(x, make_float2(SHIFT, SHIFT));
   const float2 r = fadd2(t, make_float2(-SHIFT, -SHIFT));
   const float2 f = ffma2(r, make_float2(-1.f, -1.f), x);

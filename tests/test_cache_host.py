@@ -114,6 +114,7 @@ def test_sizes(call):
 def test_other_arguments():
     inv = sdpa.SDPA_ERR_INVALID_ARG
     assert append(kr=P) == inv and append(vr=P) == inv and append(n=-1) == inv and append(n=0) == sdpa.SDPA_OK
+    assert append(kr=P, vr=FAR) == inv and append(K=FAR, kr=2 * FAR, vr=FAR + 64) == inv  # over the rows being read
     assert load(n=-1) == inv and load(n=0) == sdpa.SDPA_OK
     for call in (decode4, decode16, fwd_acc):
         for s in (NAN, INF, -INF):
