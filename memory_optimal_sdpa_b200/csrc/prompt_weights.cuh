@@ -11,8 +11,8 @@
 // after head.  MT = 2 halves the L2 traffic of the queries (32 KB per tile of 128 x 256 scores at d = 128;
 // with 128 keys all SMs together would ask for about 9 TB/s), MT = 1 is for few queries, where the keys are the
 // stream.  What bounds it: for many queries the exponentials (16 per clock and SM on the MUFU unit, so 1024
-// clocks for 128 x 128 scores, against 256 for the MMA at d = 128); every POLY_EVERY-th pair takes them on the FMA
-// pipe instead.  For few queries HBM (the keys).
+// clocks for 128 x 128 scores, against 512 for the MMA at d = 128).  For few queries the hand-offs of a unit, then HBM
+// (the keys).
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 and 3 log-sum-exps into shared memory, then softmax groups of
 // four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
@@ -35,13 +35,6 @@ struct PromptWeightsParams {
   float scale_log2;
 };
 
-#ifndef SDPA_PROMPT_POLY_EVERY
-#define SDPA_PROMPT_POLY_EVERY 8
-#endif
-#ifndef SDPA_PROMPT_GROUPS
-#define SDPA_PROMPT_GROUPS 4
-#endif
-
 template <int D, int MT>
 struct PromptCfg {
   static constexpr int TILE_BYTES = 128 * D * 2;
@@ -51,12 +44,11 @@ struct PromptCfg {
   static constexpr int NSTAGE = 512 / (128 * MT);
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KSLOT * MT * TILE_BYTES;
-  static constexpr int GROUPS = SDPA_PROMPT_GROUPS;
+  static constexpr int GROUPS = 4;  // of softmax warps (two: 394 us against 355 us for 32 heads, n = 8192, causal)
   static constexpr int TURNS = GROUPS / MT;
   static_assert(NSTAGE % TURNS == 0, "a stage belongs to one turn");
   static constexpr int LSE_OFF = Q_OFF + QSLOT * TILE_BYTES;  // [NSTAGE][128]
-  static constexpr int FLAG_OFF = LSE_OFF + NSTAGE * 128 * 4;  // [NSTAGE]: whether one of them is infinite
-  static constexpr int CNT_OFF = FLAG_OFF + 16;                // [2][TURNS][TURNS][MT * 4]: sums sent, sums collected
+  static constexpr int CNT_OFF = LSE_OFF + NSTAGE * 128 * 4;  // [2][TURNS][TURNS][MT * 4]: sums sent, sums collected
   static constexpr int CNT = TURNS * TURNS * MT * 4;
   static constexpr int SUM_OFF = CNT_OFF + 2 * CNT * 4;        // [2][TURNS][TURNS][MT * 128]
   static constexpr int BAR_OFF = SUM_OFF + 2 * TURNS * TURNS * MT * 128 * 4;
@@ -67,29 +59,10 @@ struct PromptCfg {
   static constexpr int THREADS = 128 + 128 * GROUPS;
 };
 
-// 2^x for a pair on the FMA pipe, x not NaN: as sm100::exp2_poly2 (x = j + f, 2^f by a polynomial, j into the
-// exponent), with a degree-5 polynomial (Remez exchange on [-1/2, 1/2]: relative error 7.5e-8, in fp32 2.1e-7, as
-// ex2.approx has): these weights are results, not rounded to bf16 afterwards.  Held between 2^-125 and 2^127.
-__device__ __forceinline__ float2 exp2_fine2(float2 x) {
-  using namespace sm100;
-  constexpr float SHIFT = 12582912.0f;  // 1.5 * 2^23
-  x.x = fminf(fmaxf(x.x, -125.f), 127.f);
-  x.y = fminf(fmaxf(x.y, -125.f), 127.f);
-  const float2 t = fadd2(x, make_float2(SHIFT, SHIFT));
-  const float2 r = fadd2(t, make_float2(-SHIFT, -SHIFT));
-  const float2 f = ffma2(r, make_float2(-1.f, -1.f), x);
-  float2 q = ffma2(make_float2(0x1.5c08e6p-10f, 0x1.5c08e6p-10f), f, make_float2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
-  q = ffma2(q, f, make_float2(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
-  q = ffma2(q, f, make_float2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
-  q = ffma2(q, f, make_float2(0x1.62e428p-1f, 0x1.62e428p-1f));
-  q = ffma2(q, f, make_float2(0x1.000002p+0f, 0x1.000002p+0f));
-  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
-}
-
-// The sum of 2^(s c2 - L) over 16 columns.  first: columns below it are masked (0 and less: none).
-// EVERY > 0: every EVERY-th pair on the FMA pipe, no masks and only finite exponents; 0: the form for both.
-template <int EVERY>
+// The sum of 2^(s c2 - L) over 16 columns, added to `sum` (two partial sums).  MASKED: columns below `first` count 0.
+// All exponentials on the MUFU unit: every 8th pair by a degree-5 polynomial on the FMA pipe measured 1.5 % faster for
+// many queries and slower for few, every 4th and 2nd 0 and 10 % slower for many.
+template <bool MASKED>
 __device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2, const float4* L, int first, float2 sum) {
   using namespace sm100;
   float2 a0 = make_float2(0.f, 0.f), a1 = a0;
@@ -99,16 +72,8 @@ __device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2
     const float4 l = L[i];  // minus the log-sum-exps
     const float2 x0 = ffma2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), cc, make_float2(l.x, l.y));
     const float2 x1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cc, make_float2(l.z, l.w));
-    float2 e0, e1;
-    if (EVERY > 0 && (2 * i) % (EVERY > 0 ? EVERY : 1) == 0)
-      e0 = exp2_fine2(x0);
-    else
-      e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-    if (EVERY > 0 && (2 * i + 1) % (EVERY > 0 ? EVERY : 1) == 0)
-      e1 = exp2_fine2(x1);
-    else
-      e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-    if (EVERY == 0) {  // the masked form
+    float2 e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y)), e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+    if (MASKED) {
       if (4 * i < first) e0.x = 0.f;
       if (4 * i + 1 < first) e0.y = 0.f;
       if (4 * i + 2 < first) e1.x = 0.f;
@@ -131,7 +96,6 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
   uint8_t* sK = smem + C::K_OFF;
   uint8_t* sQ = smem + C::Q_OFF;
   float* sL = (float*)(smem + C::LSE_OFF);
-  volatile int* sF = (volatile int*)(smem + C::FLAG_OFF);
   uint32_t* sent = (uint32_t*)(smem + C::CNT_OFF);  // [from turn][to turn][key warp]
   uint32_t* collected = sent + C::CNT;
   float* sums = (float*)(smem + C::SUM_OFF);
@@ -322,35 +286,29 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         v[i] = row < p.n_q ? __ldg(L + row) : -__int_as_float(0x7f800000);
       }
     };
-    int x_rows = 0, next_rows = 0;  // rows of the tile that exist
     Walk x;
     bool more = begin(x.g);
     more = settle(x, more);
     if (more && warp == 3) more = next(x);
     float v[4];
-    if (more) fetch(x, v), x_rows = p.n_q - 128 * x.qt;
+    if (more) fetch(x, v);
     for (int nq = warp - 2; more; nq += 2) {
       float next_v[4] = {};
       more = next(x) && next(x);
-      if (more) fetch(x, next_v), next_rows = p.n_q - 128 * x.qt;
+      if (more) fetch(x, next_v);
       const int st = nq % C::NSTAGE;
       bool free = true;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         free = free && mbar_wait_bounded(&s_free[st * MT + m], ((uint32_t)(nq / C::NSTAGE) & 1u) ^ 1u, abort_flag, &timed_out);
       if (!__all_sync(0xffffffffu, free)) break;
-      bool none = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float y = -1.4426950408889634f * v[i];
-        v[i] = y == __int_as_float(0x7f800000) ? -y : y;  // a query that sees no key (LSE -inf) adds nothing
-        none |= v[i] == -__int_as_float(0x7f800000) && 32 * i + lane < x_rows;
-        sL[st * 128 + 32 * i + lane] = v[i];
+        // a query that sees no key (LSE -inf) or does not exist adds nothing
+        sL[st * 128 + 32 * i + lane] = y == __int_as_float(0x7f800000) ? -y : y;
         v[i] = next_v[i];
       }
-      x_rows = next_rows;
-      none = __any_sync(0xffffffffu, none);
-      if (lane == 0) sF[st] = none;
       __syncwarp();
       if (lane < MT) mbar_arrive(&s_full[st * MT + lane]);
     }
@@ -385,8 +343,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         const float4* L = reinterpret_cast<const float4*>(sL + st * 128);
         // query row0 + c sees the key iff c >= key - off - row0
         const int first = p.causal ? key - off - row0 : 0;
-        // the exponential on the FMA pipe does not reach 0
-        const bool masked = sF[st] || (p.causal && warp_last - off - row0 > 0);
+        const bool masked = p.causal && warp_last - off - row0 > 0;
         float2 part = make_float2(0.f, 0.f);
         uint32_t s[2][16];
         tmem_ld_32x32b_x16(ta, s[0]);
@@ -396,7 +353,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
             tmem_wait_ld();
             reg_fence(s[c & 1]);
             if (c < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + 1)), s[(c + 1) & 1]);
-            part = prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[c & 1], c2, L + 4 * c, 0, part);
+            part = prompt_chunk<false>(s[c & 1], c2, L + 4 * c, 0, part);
           }
         } else {
 #pragma unroll 1
@@ -406,10 +363,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
               tmem_wait_ld();
               reg_fence(s[y]);
               if (c + y < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + y + 1)), s[y ^ 1]);
-              if (masked || 16 * (c + y + 1) > cols)
-                part = prompt_chunk<0>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), part);
-              else
-                part = prompt_chunk<SDPA_PROMPT_POLY_EVERY>(s[y], c2, L + 4 * (c + y), 0, part);
+              part = prompt_chunk<true>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), part);
             }
           tmem_wait_ld();  // the load ahead of the last columns
         }

@@ -366,6 +366,29 @@ def test_fwd_acc_with_fwd(sdpa, scale):
     assert ((acc.double().sum(-1) - seen).abs() <= 2e-3 * seen).all()
 
 
+def test_fwd_acc_nan_stays_in_its_group(sdpa):
+    """A NaN in one query reaches the weights of every key that its group's query sees, and nothing else; an infinite
+    LSE takes a query out."""
+    import torch
+    B, Hq, Hkv, n, d = 1, 4, 2, 256, 64
+    q, k, v = rnd((B, Hq, n, d), 1), rnd((B, Hkv, n, d), 2), rnd((B, Hkv, n, d), 3)
+    _, lse = sdpa.fwd(q, k.repeat_interleave(2, 1).contiguous(), v.repeat_interleave(2, 1).contiguous(), causal=True)
+    acc = sdpa.fwd_acc(q, k, lse, causal=True)
+    for row in (*range(96, 104), *range(160, 168), 255):
+        q2 = q.clone()
+        q2[0, 1, row, 7] = float("nan")
+        bad = sdpa.fwd_acc(q2, k, lse, causal=True)
+        assert torch.isnan(bad[0, 0, :row + 1]).all() and torch.equal(bad[0, 0, row + 1:], acc[0, 0, row + 1:])
+        assert torch.equal(bad[0, 1], acc[0, 1])
+    l2 = lse.clone()
+    l2[0, :, :200] = float("inf")
+    l2[0, :, 77] = -float("inf")
+    few = sdpa.fwd_acc(q, k, l2, causal=True)
+    last = sdpa.fwd_acc(q[:, :, 200:].contiguous(), k, lse[:, :, 200:].contiguous(), causal=True)
+    # the same weights, summed in another order: 56 queries of two heads
+    assert ((few - last).abs() <= 112 * 2.0 ** -23 * last).all()
+
+
 def test_fwd_acc_without_queries(sdpa):
     import torch
     k = rnd((1, 2, 7, 64), 1)
