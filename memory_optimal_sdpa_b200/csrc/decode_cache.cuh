@@ -3,7 +3,8 @@
 //
 // The keys of all (sequence, key/value head, block of query heads) units, in blocks of 64 or 128, are one long
 // line of work that is cut evenly among as many CTAs as fit on the GPU at once: lengths differ, and a
-// wave that is not full costs as much as a full one.  A CTA's cut is one or more segments, each of one unit; a segment gives
+// wave that is not full costs as much as a full one (splits of 2048 keys 183 us, two, three, four lines' worth of CTAs 168,
+// 170, 173 us against 165 us for the case below).  A CTA's cut is one or more segments, each of one unit; a segment gives
 // a normalised partial output and a log-sum-exp (base 2) per query head.  Segment number unit + CTA is unique,
 // as both only grow along the line.  With weights the scores (base 2, fp32) are written too: a key's weight
 // needs the log-sum-exp over all of its unit's segments, and 4 bytes a score, written and read once, cost far less than
@@ -13,7 +14,11 @@
 // SM's share of HBM, in which 256 codes have to become operands.  So the codes never leave registers:
 // mma.sync takes its B operand from the registers they were unpacked in, where tcgen05 would need them
 // written to shared memory as 16-bit numbers and read back (512 + 512 bytes, 8 clocks).  Measured on this
-// part: m16n8k16 one per 2.1 clocks (two a key here), integer operations two warp instructions a clock.
+// part: m16n8k16 one per 2.1 clocks (one a key here), integer operations two warp instructions a clock, of which a key
+// needs nine, six of them for the codes.  64 x 64 heads over 8, cache 16384 (713 MB): 165 us, 4.3 TB/s; the split
+// kernel alone 147 us, 8.1 clocks a key at 2.4 of 4 instructions a clock, so the instructions bound it (without them, the
+// same loads 120 us), whether 8, 12 or 16 warps share the SM (166 / 165 / 172 us).  bf16, 4 x 32 heads over 8, 32768, with
+// weights (439 MB): 86 us, 5.1 TB/s, of which the finishing kernel 12 us.
 //
 // Unpacking: (w & 0x000F000F) is, read as two fp16 numbers, c 2^-24 exactly (subnormal), and
 // (w & 0x00F000F0) 16 c 2^-24: one integer operation gives two operands.  The powers of two are put back

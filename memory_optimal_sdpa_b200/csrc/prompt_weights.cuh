@@ -8,11 +8,12 @@
 // running maximum, no exchange between threads, no atomics; the order of the sums is fixed.
 //
 // A unit of work is 128 MT keys of one (sequence, key/value head); its queries stream past in tiles of 128, head
-// after head.  MT = 2 halves the L2 traffic of the queries (32 KB per tile of 128 x 256 scores at d = 128;
-// with 128 keys all SMs together would ask for about 9 TB/s), MT = 1 is for few queries, where the keys are the
-// stream.  What bounds it: for many queries the exponentials (16 per clock and SM on the MUFU unit, so 1024
-// clocks for 128 x 128 scores, against 512 for the MMA at d = 128).  For few queries the hand-offs of a unit, then HBM
-// (the keys).
+// after head.  MT = 2 halves the waits of the producer and the MMA issuer and the L2 traffic of the queries; MT = 1 is
+// for fewer than 148 units of 256 keys.  Measured, MT = 2 against 1: 32 heads over 8, n = 8192, causal 352 and 369 us; the last 64
+// queries of 4 x 16 heads, 16001 keys, d = 64 45 and 57 us.  What bounds it: for many queries the exponentials (16
+// per clock and SM on the MUFU unit, so 1024 clocks for 128 x 128 scores, against 512 for the MMA at d = 128; 239 us for the
+// former case, whose heaviest unit is also 12 % above an SM's share).  For few queries the hand-offs of a
+// unit (about 1900 clocks in the MMA issuer), not HBM (21 us for the latter case).
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 and 3 log-sum-exps into shared memory, then softmax groups of
 // four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
