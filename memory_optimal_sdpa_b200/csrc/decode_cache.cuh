@@ -800,15 +800,15 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 }
 
 // Joins the segments of units that have several.  Grid: x < head blocks: the outputs of a unit; x beyond: the weights of
-// 1024 keys; y: key/value head; z: sequence.
+// 4096 keys; y: key/value head; z: sequence.
 constexpr int CACHE_FINISH_THREADS = 512;
-constexpr int CACHE_FINISH_KEYS = 1024;
+constexpr int CACHE_FINISH_KEYS = 4096;
 
 template <int D>
 __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel(const CacheDecodeParams p) {
   constexpr int WARPS = CACHE_FINISH_THREADS / 32;
   __shared__ float s_o[WARPS][D];
-  __shared__ float s_lse[32];
+  __shared__ float s_lse[WARPS];
   cudaGridDependencySynchronize();
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int kvh = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -885,28 +885,41 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     }
     return;
   }
-  const int j = key0 + 2 * threadIdx.x;
-  float w[2] = {0.f, 0.f};
-  for (int h0 = 0; h0 < p.group; h0 += 32) {
-    const int nh = min(32, p.group - h0);
-    __syncthreads();
-    for (int h = warp; h < nh; h += WARPS) {
-      const float x = row_lse(segments((h0 + h) / p.rows), (h0 + h) % p.rows);
-      if (lane == 0) s_lse[h] = x;
+  // Eight keys a thread, four and four.
+  float w[2][4] = {};
+  for (int h0 = 0; h0 < p.group; h0 += WARPS) {
+    const int nh = min(WARPS, p.group - h0);
+    if (h0) __syncthreads();
+    if (warp < nh) {
+      const float x = row_lse(segments((h0 + warp) / p.rows), (h0 + warp) % p.rows);
+      if (lane == 0) s_lse[warp] = x;
     }
     __syncthreads();
-    if (j < len)
-#pragma unroll 4
-      for (int h = 0; h < nh; ++h) {
-        const float2 v = *reinterpret_cast<const float2*>(p.scores + (head0 + h0 + h) * p.score_stride + j);
-        w[0] += exp2f(v.x - s_lse[h]);
-        w[1] += exp2f(v.y - s_lse[h]);
-      }
-  }
-  const size_t at = ((size_t)b * p.H_kv + kvh) * p.n_cap + j;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (j + i < len) p.acc_out[at + i] = (p.acc ? p.acc[at + i] : 0.f) + w[i];
+    for (int y = 0; y < 2; ++y) {
+      const int j = key0 + y * (CACHE_FINISH_KEYS / 2) + 4 * threadIdx.x;
+      if (j < len) {
+        const float* from = p.scores + (head0 + h0) * p.score_stride + j;
+#pragma unroll 4
+        for (int h = 0; h < nh; ++h) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(from + (size_t)h * p.score_stride));
+          const float l = s_lse[h];
+          w[y][0] += exp2f(v.x - l);
+          w[y][1] += exp2f(v.y - l);
+          w[y][2] += exp2f(v.z - l);
+          w[y][3] += exp2f(v.w - l);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int j = key0 + y * (CACHE_FINISH_KEYS / 2) + 4 * threadIdx.x;
+    const size_t at = ((size_t)b * p.H_kv + kvh) * p.n_cap + j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + i < len) p.acc_out[at + i] = (p.acc ? p.acc[at + i] : 0.f) + w[y][i];
+  }
 }
 
 }  // namespace sdpa
