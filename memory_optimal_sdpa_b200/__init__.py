@@ -353,13 +353,16 @@ def _free(t, name, dtype, ndim):
     return _tensor(t, name, dtype, (None,) * ndim).shape
 
 
+_KV4_NAMES = {name: tuple("%s.%s" % (name, x) for x in Kv4Cache._fields) for name in ("cache", "out")}
+
+
 def _kv4(cache, name="cache", B=None, H=None, d=None):
-    """Check a Kv4Cache; returns B, H, n_cap, d and its (name, tensor) pairs."""
+    """Check a Kv4Cache; returns B, H, n_cap, d."""
     import torch
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise TypeError("%s must be a Kv4Cache, got %s" % (name, type(cache).__name__))
     kc, ks, vc, vs = cache
-    names = _KV4_NAMES.get(name) or tuple("%s.%s" % (name, x) for x in Kv4Cache._fields)
+    names = _KV4_NAMES[name]
     codes = _free(kc, names[0], torch.uint8, 4)
     if B is not None and (codes[0], codes[1], 2 * codes[3]) != (B, H, d):
         _tensor(kc, names[0], torch.uint8, (B, H, None, d // 2))
@@ -368,10 +371,19 @@ def _kv4(cache, name="cache", B=None, H=None, d=None):
     _fit(ks, names[1], torch.bfloat16, scales)
     _fit(vc, names[2], torch.uint8, codes)
     _fit(vs, names[3], torch.bfloat16, scales)
-    return B, H, n_cap, 2 * half, ((names[0], kc), (names[1], ks), (names[2], vc), (names[3], vs))
+    return B, H, n_cap, 2 * half
 
 
-_KV4_NAMES = {name: tuple("%s.%s" % (name, x) for x in Kv4Cache._fields) for name in ("cache", "out")}
+def _here(names, *tensors):
+    """_device for tensors named by `names`."""
+    index = tensors[0].get_device()  # -1: on the host
+    if index >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return tensors[0].device
+    return _device(names[0], tensors[0], *zip(names[1:], tensors[1:]))
 
 
 def _both(name, a, b):
@@ -395,13 +407,14 @@ def _at(t):
 def _launch(where, dev, stream, *args):
     """Call the library function `where` with these arguments and the stream, `dev` being current."""
     import torch
+    index = dev.index
     if stream is None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
+        handle = raw(index) if raw else torch.cuda.current_stream(dev).cuda_stream
     else:
         handle = _stream(stream, dev)
     fn = getattr(lib, where)
-    if torch.cuda.current_device() == dev.index:
+    if torch.cuda.current_device() == index:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -416,7 +429,7 @@ def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, strea
     changed.  k_read, v_read (both or neither, shapes of k, v) receive the values the cache now stands for."""
     import torch
     bf, i32 = torch.bfloat16, torch.int32
-    B, H, n_cap, d, parts = _kv4(cache)
+    B, H, n_cap, d = _kv4(cache)
     rows = _free(k, "k", bf, 4)
     _fit(k, "k", bf, (B, H, rows[2], d))
     _fit(v, "v", bf, rows)
@@ -427,10 +440,11 @@ def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, strea
     if k_read is not None:
         _fit(k_read, "k_read", bf, rows)
         _fit(v_read, "v_read", bf, rows)
-    dev = _device("k", k, ("v", v), ("kv_lens", kv_lens), ("n_new", n_new), ("k_read", k_read), ("v_read", v_read),
-                  *parts)
-    _launch("sdpa_kv4_append", dev, stream, _at(k), _at(v), _at(kv_lens), _at(n_new), *map(_at, cache), _at(k_read),
-            _at(v_read), B, H, rows[2], n_cap, d)
+    kc, ks, vc, vs = cache
+    dev = _here(("k", "v", "kv_lens", "n_new", "k_read", "v_read") + _KV4_NAMES["cache"], k, v, kv_lens, n_new, k_read, v_read,
+                kc, ks, vc, vs)
+    _launch("sdpa_kv4_append", dev, stream, k.data_ptr(), v.data_ptr(), kv_lens.data_ptr(), _at(n_new), kc.data_ptr(),
+            ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), _at(k_read), _at(v_read), B, H, rows[2], n_cap, d)
 
 
 def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
@@ -438,20 +452,22 @@ def kv4_load(cache, kv_lens, n_rows=None, k=None, v=None, stream=None):
     are given, else n_cap.  Rows past a sequence's length are left as they were (zero in tensors made here)."""
     import torch
     bf = torch.bfloat16
-    B, H, n_cap, d, parts = _kv4(cache)
+    B, H, n_cap, d = _kv4(cache)
     _both("k and v", k, v)
     if k is not None:
         n_rows = _free(k, "k", bf, 4)[2] if n_rows is None else n_rows
         _fit(k, "k", bf, (B, H, n_rows, d))
         _fit(v, "v", bf, (B, H, n_rows, d))
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
-    dev = _device("cache.k_codes", cache[0], *parts[1:], ("kv_lens", kv_lens), ("k", k), ("v", v))
+    kc, ks, vc, vs = cache
+    dev = _here(_KV4_NAMES["cache"] + ("kv_lens", "k", "v"), kc, ks, vc, vs, kv_lens, k, v)
     n_rows = n_cap if n_rows is None else n_rows
     if n_rows < 0:
         raise ValueError("n_rows must not be negative, got %d" % n_rows)
     if k is None:
         k, v = _made(stream, lambda: [torch.zeros((B, H, n_rows, d), dtype=bf, device=dev) for _ in "kv"])
-    _launch("sdpa_kv4_load", dev, stream, *map(_at, cache), _at(kv_lens), _at(k), _at(v), B, H, n_rows, n_cap, d)
+    _launch("sdpa_kv4_load", dev, stream, kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), kv_lens.data_ptr(),
+            k.data_ptr(), v.data_ptr(), B, H, n_rows, n_cap, d)
     return k, v
 
 
@@ -466,10 +482,9 @@ def _acc_args(acc, acc_out, shape):
     return acc if acc_out is None else acc_out
 
 
-def _decode_run(where, size, q, keys, parts, kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
-                workspace, stream):
-    """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size` the workspace's bytes for
-    a number of query heads."""
+def _decode_run(where, size, q, keys, names, kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace,
+                stream):
+    """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size(H_q)` the workspace's bytes."""
     import torch
     H_q = _free(q, "q", torch.bfloat16, 3)[1]
     _fit(q, "q", torch.bfloat16, (B, H_q, d))
@@ -478,17 +493,17 @@ def _decode_run(where, size, q, keys, parts, kv_lens, B, H_kv, n_cap, d, scale, 
         _fit(o, "o", torch.bfloat16, q.shape)
     if lse is not None:
         _fit(lse, "lse", torch.float32, (B, H_q))
-    dev = _device("q", q, ("kv_lens", kv_lens), ("o", o), ("lse", lse), ("acc", acc), ("acc_out", acc_out), *parts)
+    dev = _here(("q", "kv_lens", "o", "lse", "acc", "acc_out") + names, q, kv_lens, o, lse, acc, acc_out, *keys)
 
     def outputs():
         return (torch.empty_like(q) if o is None else o,
-                torch.empty((B, H_q), dtype=torch.float32, device=dev) if lse is None and want_lse else lse,
+                q.new_empty((B, H_q), dtype=torch.float32) if lse is None and want_lse else lse,
                 torch.empty(max(size(H_q), 16), dtype=torch.uint8, device=dev) if workspace is None
                 else _workspace(workspace, 0, dev))
-    o, lse, ws = _made(stream, outputs)
+    o, lse, ws = outputs() if stream is None else _made(stream, outputs)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    _launch(where, dev, stream, _at(q), *map(_at, keys), _at(kv_lens), _at(o), _at(lse), _at(acc), _at(acc_out), B, H_q,
-            H_kv, n_cap, d, scale, _at(ws), _nbytes(ws))
+    _launch(where, dev, stream, q.data_ptr(), *[t.data_ptr() for t in keys], kv_lens.data_ptr(), o.data_ptr(), _at(lse),
+            _at(acc), _at(acc_out), B, H_q, H_kv, n_cap, d, scale, ws.data_ptr(), _nbytes(ws))
     return o, lse
 
 
@@ -503,11 +518,12 @@ def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, a
     [B] on the device (0: an empty slot, O = 0 and LSE = -inf).  With acc [B,H_kv,n_cap] fp32, each cached key's
     weights, summed over the query heads that read it, are added: acc_out = acc + weights (in place without acc_out;
     acc_out alone starts from zero); entries past kv_lens are left as they were."""
-    B, H_kv, n_cap, d, parts = _kv4(cache)
-    acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
+    B, H_kv, n_cap, d = _kv4(cache)
+    if acc is not None or acc_out is not None:
+        acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
     return _decode_run("sdpa_decode_kv4",
-                       lambda H_q: decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), q, cache, parts,
-                       kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
+                       lambda H_q: decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), q, cache,
+                       _KV4_NAMES["cache"], kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -526,7 +542,7 @@ def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse
         raise ValueError("give acc, acc_out or both")
     acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
     return _decode_run("sdpa_decode_acc", lambda H_q: decode_acc_workspace_size(B, H_q, H_kv, n_cap, d), q, (k, v),
-                       (("k", k), ("v", v)), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
+                       ("k", "v"), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
                        workspace, stream)
 
 
@@ -542,34 +558,38 @@ def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=
     _fit(k, "k", torch.bfloat16, (B, H_kv, n_kv, d))
     _fit(lse, "lse", torch.float32, (B, H_q, n_q))
     acc_out = _acc_args(acc, acc_out, (B, H_kv, None))
-    dev = _device("q", q, ("k", k), ("lse", lse), ("acc", acc), ("acc_out", acc_out))
+    dev = _here(("q", "k", "lse", "acc", "acc_out"), q, k, lse, acc, acc_out)
     if acc_out is None:
         acc_out = _made(stream, lambda: torch.empty((B, H_kv, n_kv), dtype=torch.float32, device=dev))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    _launch("sdpa_fwd_acc", dev, stream, _at(q), _at(k), _at(lse), _at(acc), _at(acc_out), B, H_q, H_kv, n_q, n_kv,
+    _launch("sdpa_fwd_acc", dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), _at(acc), acc_out.data_ptr(), B, H_q, H_kv, n_q, n_kv,
             acc_out.shape[2], d, scale, int(bool(causal)))
     return acc_out
 
 
-def _evict_run(where, arrays, outs, in_parts, out_parts, out_name, acc, kv_lens, budget, recent, acc_out, B, H, n_cap,
-               n_out, d, stream):
+def _evict_run(where, arrays, outs, names, out_names, acc, kv_lens, budget, recent, acc_out, B, H, n_cap, n_out, d, stream):
     """The part that evict and kv4_evict share; outs None: in place."""
     import torch
     budget, recent = int(budget), int(recent)
     _fit(acc, "acc", torch.float32, (B, H, n_cap))
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
     if (outs is None) != (acc_out is None):
-        raise ValueError("give %s and acc_out together, or none of them (in place)" % out_name)
+        raise ValueError("give %s and acc_out together, or none of them (in place)" % ", ".join(out_names))
     if acc_out is not None:
         _fit(acc_out, "acc_out", torch.float32, (B, H, n_out))
-    name, ref = in_parts[0]
-    dev = _device(name, ref, *in_parts[1:], *out_parts, ("acc", acc), ("kv_lens", kv_lens), ("acc_out", acc_out))
+        dev = _here(names + ("acc", "kv_lens", "acc_out") + out_names, *arrays, acc, kv_lens, acc_out, *outs)
+    else:
+        outs, acc_out = arrays, acc
+        dev = _here(names + ("acc", "kv_lens"), *arrays, acc, kv_lens)
     if not 1 <= budget <= n_out:
         raise ValueError("budget must be between 1 and the output's capacity %d, got %d" % (n_out, budget))
-    keep, new_lens = _made(stream, lambda: (torch.empty((B, H, budget), dtype=torch.int32, device=dev),
-                                            torch.empty((B,), dtype=torch.int32, device=dev)))
-    _launch(where, dev, stream, *map(_at, arrays), _at(acc), _at(kv_lens), *map(_at, arrays if outs is None else outs),
-            _at(acc if acc_out is None else acc_out), _at(keep), _at(new_lens), B, H, n_cap, n_out, d, budget, recent)
+
+    def results():
+        return kv_lens.new_empty((B, H, budget)), torch.empty_like(kv_lens)
+    keep, new_lens = results() if stream is None else _made(stream, results)
+    _launch(where, dev, stream, *[t.data_ptr() for t in arrays], acc.data_ptr(), kv_lens.data_ptr(),
+            *[t.data_ptr() for t in outs], acc_out.data_ptr(), keep.data_ptr(), new_lens.data_ptr(), B, H, n_cap, n_out, d,
+            budget, recent)
     return keep, new_lens
 
 
@@ -583,23 +603,21 @@ def evict(k, v, acc, kv_lens, budget, recent=0, k_out=None, v_out=None, acc_out=
     B, H, n_cap, d = _free(k, "k", bf, 4)
     _fit(v, "v", bf, k.shape)
     _both("k_out and v_out", k_out, v_out)
-    n_out, outs, out_parts = n_cap, None, ()
+    n_out, outs = n_cap, None
     if k_out is not None:
-        _tensor(k_out, "k_out", bf, (B, H, None, d))
-        n_out, outs, out_parts = k_out.shape[2], (k_out, v_out), (("k_out", k_out), ("v_out", v_out))
+        n_out, outs = _free(k_out, "k_out", bf, 4)[2], (k_out, v_out)
+        _fit(k_out, "k_out", bf, (B, H, n_out, d))
         _fit(v_out, "v_out", bf, k_out.shape)
-    return _evict_run("sdpa_evict", (k, v), outs, (("k", k), ("v", v)), out_parts, "k_out, v_out", acc, kv_lens, budget,
-                      recent, acc_out, B, H, n_cap, n_out, d, stream)
+    return _evict_run("sdpa_evict", (k, v), outs, ("k", "v"), ("k_out", "v_out"), acc, kv_lens, budget, recent, acc_out, B, H,
+                      n_cap, n_out, d, stream)
 
 
 def kv4_evict(cache, acc, kv_lens, budget, recent=0, out=None, acc_out=None, stream=None):
     """evict for a 4-bit cache: in place, or into the cache `out` (any capacity >= budget) and acc_out."""
-    B, H, n_cap, d, parts = _kv4(cache)
-    n_out, out_parts = n_cap, ()
-    if out is not None:
-        _, _, n_out, _, out_parts = _kv4(out, "out", B, H, d)
-    return _evict_run("sdpa_kv4_evict", cache, out, parts, out_parts, "out", acc, kv_lens, budget, recent, acc_out, B, H,
-                      n_cap, n_out, d, stream)
+    B, H, n_cap, d = _kv4(cache)
+    n_out = n_cap if out is None else _kv4(out, "out", B, H, d)[2]
+    return _evict_run("sdpa_kv4_evict", cache, out, _KV4_NAMES["cache"], _KV4_NAMES["out"], acc, kv_lens, budget, recent,
+                      acc_out, B, H, n_cap, n_out, d, stream)
 
 
 def get_last_device_error(stream=None):
