@@ -482,9 +482,22 @@ def _acc_args(acc, acc_out, shape):
     return acc if acc_out is None else acc_out
 
 
+def _decode_made(q, o, lse, want_lse, workspace, need, dev):
+    """The outputs and the workspace of a decode, those not given made on the current stream."""
+    import torch
+    if o is None:
+        o = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    if workspace is None:
+        return o, lse, q.new_empty(max(need, 16), dtype=torch.uint8)
+    return o, lse, _workspace(workspace, 0, dev)
+
+
 def _decode_run(where, size, q, keys, names, kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace,
                 stream):
-    """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size(H_q)` the workspace's bytes."""
+    """The part that decode_kv4 and decode_acc share: `keys` are the cache's arrays, `size` the function that gives the
+    workspace's bytes."""
     import torch
     H_q = _free(q, "q", torch.bfloat16, 3)[1]
     _fit(q, "q", torch.bfloat16, (B, H_q, d))
@@ -494,13 +507,12 @@ def _decode_run(where, size, q, keys, names, kv_lens, B, H_kv, n_cap, d, scale, 
     if lse is not None:
         _fit(lse, "lse", torch.float32, (B, H_q))
     dev = _here(("q", "kv_lens", "o", "lse", "acc", "acc_out") + names, q, kv_lens, o, lse, acc, acc_out, *keys)
-
-    def outputs():
-        return (torch.empty_like(q) if o is None else o,
-                q.new_empty((B, H_q), dtype=torch.float32) if lse is None and want_lse else lse,
-                torch.empty(max(size(H_q), 16), dtype=torch.uint8, device=dev) if workspace is None
-                else _workspace(workspace, 0, dev))
-    o, lse, ws = outputs() if stream is None else _made(stream, outputs)
+    need = size(B, H_q, H_kv, n_cap, d, acc_out is not None) if workspace is None else 0
+    if stream is None:
+        o, lse, ws = _decode_made(q, o, lse, want_lse, workspace, need, dev)
+    else:
+        with torch.cuda.stream(stream):
+            o, lse, ws = _decode_made(q, o, lse, want_lse, workspace, need, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     _launch(where, dev, stream, q.data_ptr(), *[t.data_ptr() for t in keys], kv_lens.data_ptr(), o.data_ptr(), _at(lse),
             _at(acc), _at(acc_out), B, H_q, H_kv, n_cap, d, scale, ws.data_ptr(), _nbytes(ws))
@@ -521,14 +533,16 @@ def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, a
     B, H_kv, n_cap, d = _kv4(cache)
     if acc is not None or acc_out is not None:
         acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    return _decode_run("sdpa_decode_kv4",
-                       lambda H_q: decode_kv4_workspace_size(B, H_q, H_kv, n_cap, d, acc_out is not None), q, cache,
-                       _KV4_NAMES["cache"], kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
+    return _decode_run("sdpa_decode_kv4", decode_kv4_workspace_size, q, cache, _KV4_NAMES["cache"], kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
 
 
 @functools.lru_cache(maxsize=256)
 def decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d):
     return int(lib.sdpa_decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d))
+
+
+def _decode_acc_size(batch, heads_q, heads_kv, n_kv_cap, d, with_acc):
+    return decode_acc_workspace_size(batch, heads_q, heads_kv, n_kv_cap, d)
 
 
 def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse=None, want_lse=True, workspace=None,
@@ -541,8 +555,7 @@ def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse
     if acc is None and acc_out is None:
         raise ValueError("give acc, acc_out or both")
     acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    return _decode_run("sdpa_decode_acc", lambda H_q: decode_acc_workspace_size(B, H_q, H_kv, n_cap, d), q, (k, v),
-                       ("k", "v"), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
+    return _decode_run("sdpa_decode_acc", _decode_acc_size, q, (k, v), ("k", "v"), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
                        workspace, stream)
 
 

@@ -512,6 +512,42 @@ def test_serving_run(sdpa, d, G):
     assert ((O.double() - ref).abs() <= 1e-2 + 1e-2 * ref.abs()).all()
 
 
+def test_given_outputs_workspace_and_stream(sdpa):
+    """Outputs, workspaces and a stream from the caller give what the plain calls give; a workspace too small is refused."""
+    import torch
+    B, Hq, Hkv, cap, d, lens = 2, 12, 4, 500, 128, [500, 77]
+    q, kv, vv = rnd((B, Hq, d), 1), rnd((B, Hkv, cap, d), 2), rnd((B, Hkv, cap, d), 3)
+    c = random_cache(sdpa, B, Hkv, cap, d, lens, 4)
+    acc = rnd((B, Hkv, cap), 5).float()
+    n = i32(lens)
+    side = torch.cuda.Stream()
+    for call, size in ((lambda **kw: sdpa.decode_kv4(q, c, n, acc=acc, **kw), sdpa.decode_kv4_workspace_size(B, Hq, Hkv, cap, d, True)),
+                       (lambda **kw: sdpa.decode_acc(q, kv, vv, n, acc, **kw), sdpa.decode_acc_workspace_size(B, Hq, Hkv, cap, d))):
+        out = torch.zeros_like(acc)
+        O, L = call(acc_out=out)
+        o, lse, ws = torch.empty_like(q), torch.empty((B, Hq), device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda")
+        out2 = torch.zeros_like(acc)
+        torch.cuda.synchronize()
+        O2, L2 = call(o=o, lse=lse, workspace=ws, acc_out=out2, stream=side)
+        side.synchronize()
+        assert O2 is o and L2 is lse and torch.equal(O, O2) and torch.equal(L, L2) and torch.equal(out, out2)
+        out3 = torch.zeros_like(acc)
+        torch.cuda.synchronize()
+        O3, L3 = call(acc_out=out3, stream=side)
+        side.synchronize()
+        assert torch.equal(O, O3) and torch.equal(L, L3) and torch.equal(out, out3)
+        with pytest.raises(sdpa.SdpaError, match="WORKSPACE"):
+            call(acc_out=out, workspace=ws[:-16])
+    torch.cuda.synchronize()
+    k, v = sdpa.kv4_load(c, n, stream=side)
+    side.synchronize()
+    assert torch.equal(k, sdpa.kv4_load(c, n)[0])
+    w = sdpa.fwd_acc(q[:, :, None].contiguous(), kv, L[:, :, None].contiguous(), stream=side)
+    keep, new = sdpa.kv4_evict(c, acc.clone(), n, 60, recent=7, stream=side)
+    side.synchronize()
+    assert w.shape == (B, Hkv, cap) and new.tolist() == [60, 60] and keep[1, 0, -7:].tolist() == list(range(70, 77))
+
+
 def test_streams_and_graphs(sdpa):
     """A decode step captured once and replayed as the cache grows, beside eager calls on another stream."""
     import torch
