@@ -15,7 +15,7 @@
  * as SDPA_ERR_DEVICE_BAD_LENGTH), batch == 0 or heads == 0 -> SDPA_OK.  d is 64 or 128, else
  * SDPA_ERR_UNSUPPORTED.  Unlike sdpa_decode, lengths may be 0 here (an empty slot of a padded batch).
  * int32 and float arrays (lengths, LSE, weights, kept rows) need 4-byte alignment only.
- * batch * heads * rows of every array is below 2^31, batch and heads are at most 65535.
+ * batch * heads * rows of every array is at most 2^31 - 8192, batch and heads are at most 65535.
  *
  * The 4-bit row.  The d channels form NG = d / 32 groups of 32.  Group g has a scale s and a minimum m,
  * both bf16, and a code c in 0 .. 15 for each channel, which stands for the number s c + m.
@@ -73,7 +73,8 @@ SDPA_API int sdpa_kv4_load(const void* k_codes, const void* k_scales, const void
  *     acc_out[b, g, j] = acc[b, g, j] + sum over the query heads h of group g of exp(scale q_h . k_j - LSE_h)
  * for j < kv_lens[b]; entries at or past kv_lens[b] are left as they were.  acc may be acc_out (the usual
  * running sum) or NULL (zeros); acc without acc_out is SDPA_ERR_INVALID_ARG.
- * workspace: sdpa_decode_kv4_workspace_size bytes (with_acc: whether acc_out is given), scratch.
+ * workspace: sdpa_decode_kv4_workspace_size bytes (with_acc: whether acc_out is given), scratch.  Calls that may run at
+ * the same time (other streams, graphs replayed side by side) need one each.
  */
 SDPA_API size_t sdpa_decode_kv4_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d, int with_acc);
 SDPA_API int sdpa_decode_kv4(const void* Q, const void* k_codes, const void* k_scales, const void* v_codes,

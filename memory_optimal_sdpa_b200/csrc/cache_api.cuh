@@ -14,9 +14,10 @@ namespace {
 
 bool cache_head_dim(int d) { return d == 64 || d == 128; }
 
-// batch, heads and batch * heads * rows within what the kernels index with 32 bits.
+// batch, heads and batch * heads * rows within what the kernels index with 32 bits.  They round row numbers up to whole
+// blocks of 4096 at most, and step on by one more, before they compare them with a length.
 bool cache_sizes_fit(long long batch, long long heads, long long rows) {
-  return batch <= 65535 && heads <= 65535 && batch * heads * rows < (1LL << 31);
+  return batch <= 65535 && heads <= 65535 && batch * heads * rows <= (1LL << 31) - 8192;
 }
 
 int launched(const char* what) {
@@ -278,9 +279,8 @@ extern "C" int sdpa_decode_acc(const void* Q, const void* K, const void* V, cons
 // ------------------------------------------------------------------ weights of a prompt
 namespace {
 
-// Units of 256 keys where every unit has at least eight query tiles to stream past them and there is a unit
-// for every SM; else of 128.
-bool prompt_wide(const sdpa::PromptWeightsParams& p, int) {
+// Units of 256 keys where there is one for every SM, else of 128 (both measured at the head of prompt_weights.cuh).
+bool prompt_wide(const sdpa::PromptWeightsParams& p) {
   return (long long)p.bkv * ((p.n_kv + 255) / 256) >= 148;
 }
 
@@ -331,7 +331,7 @@ extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, cons
   p.bkv = batch * heads_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = (cudaStream_t)stream;
-  const bool wide = prompt_wide(p, batch);
+  const bool wide = prompt_wide(p);
   if (d == 64) return wide ? launch_prompt_weights<64, 2>(Q, K, p, batch, s) : launch_prompt_weights<64, 1>(Q, K, p, batch, s);
   return wide ? launch_prompt_weights<128, 2>(Q, K, p, batch, s) : launch_prompt_weights<128, 1>(Q, K, p, batch, s);
 }

@@ -111,6 +111,16 @@ def test_sizes(call):
         assert call(b=65535, hq=64, hkv=64, nkv=1 << 20, nacc=1 << 20) == sdpa.SDPA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("call", CALLS)
+def test_rows_that_would_pass_32_bits_when_rounded_up(call):
+    """2^31 - 8192 rows are the most: row numbers are rounded up to blocks in 32 bits."""
+    most = (1 << 31) - 8192
+    sizes = {"hq": 1, "nkv": most + 1, "nacc": most + 1} if call is fwd_acc else {"cap": most + 1}
+    if call in (decode4, decode16):
+        sizes.update(hq=1, nbytes=1 << 62)
+    assert call(**sizes) == sdpa.SDPA_ERR_UNSUPPORTED
+
+
 def test_other_arguments():
     inv = sdpa.SDPA_ERR_INVALID_ARG
     assert append(kr=P) == inv and append(vr=P) == inv and append(n=-1) == inv and append(n=0) == sdpa.SDPA_OK
