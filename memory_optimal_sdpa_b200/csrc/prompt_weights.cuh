@@ -60,11 +60,13 @@ struct PromptCfg {
   static constexpr int THREADS = 128 + 128 * GROUPS;
 };
 
-// The sum of 2^(s c2 - L) over 16 columns, added to `sum` (two partial sums).  MASKED: columns below `first` count 0.
+// The sum of 2^(s c2 - L) over 16 columns, added to `sum` (two partial sums).  MASKED: columns below `first` and from `end`
+// on count 0, whatever their scores are (a row of zeros that stands for no query gives NaN with an infinite key).
 // All exponentials on the MUFU unit: every 8th pair by a degree-5 polynomial on the FMA pipe measured 1.5 % faster for
 // many queries and slower for few, every 4th and 2nd 0 and 10 % slower for many.
 template <bool MASKED>
-__device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2, const float4* L, int first, float2 sum) {
+__device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2, const float4* L, int first, int end,
+                                               float2 sum) {
   using namespace sm100;
   float2 a0 = make_float2(0.f, 0.f), a1 = a0;
   const float2 cc = make_float2(c2, c2);
@@ -75,10 +77,10 @@ __device__ __forceinline__ float2 prompt_chunk(const uint32_t (&s)[16], float c2
     const float2 x1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), cc, make_float2(l.z, l.w));
     float2 e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y)), e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
     if (MASKED) {
-      if (4 * i < first) e0.x = 0.f;
-      if (4 * i + 1 < first) e0.y = 0.f;
-      if (4 * i + 2 < first) e1.x = 0.f;
-      if (4 * i + 3 < first) e1.y = 0.f;
+      if (4 * i < first || 4 * i >= end) e0.x = 0.f;
+      if (4 * i + 1 < first || 4 * i + 1 >= end) e0.y = 0.f;
+      if (4 * i + 2 < first || 4 * i + 2 >= end) e1.x = 0.f;
+      if (4 * i + 3 < first || 4 * i + 3 >= end) e1.y = 0.f;
     }
     a0 = fadd2(a0, e0);
     a1 = fadd2(a1, e1);
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
             tmem_wait_ld();
             reg_fence(s[c & 1]);
             if (c < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + 1)), s[(c + 1) & 1]);
-            part = prompt_chunk<false>(s[c & 1], c2, L + 4 * c, 0, part);
+            part = prompt_chunk<false>(s[c & 1], c2, L + 4 * c, 0, 16, part);
           }
         } else {
 #pragma unroll 1
@@ -364,7 +366,10 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
               tmem_wait_ld();
               reg_fence(s[y]);
               if (c + y < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + y + 1)), s[y ^ 1]);
-              part = prompt_chunk<true>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), part);
+              if (!masked && 16 * (c + y + 1) <= cols)
+                part = prompt_chunk<false>(s[y], c2, L + 4 * (c + y), 0, 16, part);
+              else
+                part = prompt_chunk<true>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), cols - 16 * (c + y), part);
             }
           tmem_wait_ld();  // the load ahead of the last columns
         }

@@ -389,6 +389,27 @@ def test_fwd_acc_nan_stays_in_its_group(sdpa):
     assert ((few - last).abs() <= 112 * 2.0 ** -23 * last).all()
 
 
+@pytest.mark.parametrize("n_q", [1, 40, 64, 129])
+@pytest.mark.parametrize("causal", [False, True])
+def test_fwd_acc_key_of_minus_infinity(sdpa, n_q, causal):
+    """A key whose scores are all -inf weighs 0 and changes nothing else, for any number of queries."""
+    import torch
+    n_kv, d = 200, 64
+    q, k = rnd((1, 4, n_q, d), 1), rnd((1, 2, n_kv, d), 2)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    s = torch.einsum("bhgid,bhjd->bhgij", q.double().view(1, 2, 2, n_q, d), k.double()) / 8
+    s[..., 30] = -math.inf
+    if causal:
+        s.masked_fill_(torch.arange(n_kv, device="cuda") > torch.arange(n_q, device="cuda")[:, None] + (n_kv - n_q), -math.inf)
+    lse = torch.logsumexp(s, -1).float().view(1, 4, n_q)
+    plain = sdpa.fwd_acc(q, k, lse, causal=causal)
+    k[:, :, 30, 5] = -math.inf
+    acc = sdpa.fwd_acc(q, k, lse, causal=causal)
+    assert (acc[..., 30] == 0).all()
+    acc[..., 30] = plain[..., 30]
+    assert torch.equal(acc, plain)
+
+
 def test_fwd_acc_without_queries(sdpa):
     import torch
     k = rnd((1, 2, 7, 64), 1)
