@@ -533,7 +533,8 @@ def decode_kv4(q, cache, kv_lens, scale=None, o=None, lse=None, want_lse=True, a
     B, H_kv, n_cap, d = _kv4(cache)
     if acc is not None or acc_out is not None:
         acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    return _decode_run("sdpa_decode_kv4", decode_kv4_workspace_size, q, cache, _KV4_NAMES["cache"], kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
+    return _decode_run("sdpa_decode_kv4", decode_kv4_workspace_size, q, cache, _KV4_NAMES["cache"], kv_lens, B, H_kv,
+                       n_cap, d, scale, o, lse, want_lse, acc, acc_out, workspace, stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -555,8 +556,8 @@ def decode_acc(q, k, v, kv_lens, acc=None, acc_out=None, scale=None, o=None, lse
     if acc is None and acc_out is None:
         raise ValueError("give acc, acc_out or both")
     acc_out = _acc_args(acc, acc_out, (B, H_kv, n_cap))
-    return _decode_run("sdpa_decode_acc", _decode_acc_size, q, (k, v), ("k", "v"), kv_lens, B, H_kv, n_cap, d, scale, o, lse, want_lse, acc, acc_out,
-                       workspace, stream)
+    return _decode_run("sdpa_decode_acc", _decode_acc_size, q, (k, v), ("k", "v"), kv_lens, B, H_kv, n_cap, d, scale, o,
+                       lse, want_lse, acc, acc_out, workspace, stream)
 
 
 def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=None):
@@ -575,8 +576,8 @@ def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=
     if acc_out is None:
         acc_out = _made(stream, lambda: torch.empty((B, H_kv, n_kv), dtype=torch.float32, device=dev))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    _launch("sdpa_fwd_acc", dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), _at(acc), acc_out.data_ptr(), B, H_q, H_kv, n_q, n_kv,
-            acc_out.shape[2], d, scale, int(bool(causal)))
+    _launch("sdpa_fwd_acc", dev, stream, q.data_ptr(), k.data_ptr(), lse.data_ptr(), _at(acc), acc_out.data_ptr(),
+            B, H_q, H_kv, n_q, n_kv, acc_out.shape[2], d, scale, int(bool(causal)))
     return acc_out
 
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "sdpa_cache.h"
 #include "decode_cache.cuh"
@@ -22,6 +23,24 @@ bool cache_sizes_fit(long long batch, long long heads, long long rows) {
 
 int launched(const char* what) {
   const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SDPA_OK : cuda_fail(what, e);
+}
+
+// A programmatic dependent of the launch before it: its own launch overlaps that one's last wave, and the kernel waits for it
+// (cudaGridDependencySynchronize) before it reads anything.
+template <class Params>
+int launch_dependent(const char* what, void (*kern)(Params), dim3 grid, int threads, cudaStream_t s,
+                     const std::remove_const_t<Params>& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   return e == cudaSuccess ? SDPA_OK : cuda_fail(what, e);
 }
 
@@ -181,19 +200,10 @@ int launch_cache_decode(sdpa::CacheDecodeParams p, cudaStream_t s) {
   if (most < p.n_cta) p.n_cta = (int)most;
   const int rc = wide ? launch_cache_split<D, KV4, true>(p, s) : launch_cache_split<D, KV4, false>(p, s);
   if (rc != SDPA_OK) return rc;
-  // a programmatic dependent: its launch overlaps the splits' last wave, and it waits for them itself
-  cudaLaunchConfig_t cfg = {};
   const int key_blocks = p.scores ? (p.n_cap + sdpa::CACHE_FINISH_KEYS - 1) / sdpa::CACHE_FINISH_KEYS : 0;
-  cfg.gridDim = dim3((unsigned)(p.head_blocks + key_blocks), (unsigned)p.H_kv, (unsigned)p.B);
-  cfg.blockDim = dim3(sdpa::CACHE_FINISH_THREADS);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, sdpa::sdpa_cache_finish_kernel<D>, p);
-  return e == cudaSuccess ? SDPA_OK : cuda_fail("cache decode finish launch", e);
+  return launch_dependent("cache decode finish launch", sdpa::sdpa_cache_finish_kernel<D>,
+                          dim3((unsigned)(p.head_blocks + key_blocks), (unsigned)p.H_kv, (unsigned)p.B),
+                          sdpa::CACHE_FINISH_THREADS, s, p);
 }
 
 // The part that both decodes share: p holds the cache; everything else is checked and filled in here.
@@ -402,15 +412,17 @@ int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens,
     r.n_bh = (int)bh;
     if (in_place) {
       const dim3 grid((unsigned)bh, (unsigned)((largest + 63) / 64), (unsigned)k);
-      sdpa::sdpa_evict_rows_in_place_kernel<<<grid, sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
+      if (int e = launch_dependent("evict rows launch", sdpa::sdpa_evict_rows_in_place_kernel, grid, sdpa::EVICT_ROW_THREADS, s, r))
+        return e;
     } else {
       // four blocks an SM in all, no more than stretches of the array with the longest rows
       const long long rows = sdpa::EVICT_ROW_THREADS * sdpa::EVICT_ROW_UNROLL * 16 / (long long)largest;
       long long blocks = (budget + rows - 1) / rows * (long long)bh;
       if (blocks > 148 * 4 / k) blocks = 148 * 4 / k;
-      sdpa::sdpa_evict_rows_kernel<<<dim3((unsigned)blocks, (unsigned)k), sdpa::EVICT_ROW_THREADS, 0, s>>>(r);
+      if (int e = launch_dependent("evict rows launch", sdpa::sdpa_evict_rows_kernel, dim3((unsigned)blocks, (unsigned)k),
+                                   sdpa::EVICT_ROW_THREADS, s, r))
+        return e;
     }
-    if (int e = launched("evict rows launch")) return e;
   }
   return SDPA_OK;
 }
