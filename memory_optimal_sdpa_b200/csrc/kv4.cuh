@@ -90,14 +90,55 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The codes of this thread's eight channels (as floats and packed), and the group's scale (bits 0 .. 15) and minimum.
-// The four threads of a group are lanes differing in bits 0 and 1.
-__device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scale, float (&code)[8]) {
+// Lane-wise product of two pairs.
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// The codes (as floats, and packed) of eight channels x of a group with minimum lo and scale s, inv its reciprocal.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], float lo, float s, float inv, float (&code)[8]) {
+  float t[8], far = 0.f;
+  constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to a whole number, halves to even
+  const float2 low = make_float2(-lo, -lo), up = make_float2(ROUND, ROUND), back = make_float2(-ROUND, -ROUND);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {  // in pairs: half the instructions
+    const float2 q = fmul2(sm100::fadd2(make_float2(x[i], x[i + 1]), low), make_float2(inv, inv));  // within 1e-5 of the quotients
+    const float2 c = sm100::fadd2(sm100::fadd2(q, up), back);
+    const float2 off = sm100::ffma2(c, make_float2(-1.f, -1.f), q);
+    t[i] = q.x, t[i + 1] = q.y, code[i] = c.x, code[i + 1] = c.y;
+    far = sm100::max3f(far, fabsf(off.x), fabsf(off.y));
+  }
+  if (far > 0.49998f) {  // one of them is near a half
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(t[i] - code[i]) > 0.49998f) code[i] = kv4_code_exact(x[i], lo, s, code[i]);
+  }
+  // 16-bit pieces as whole numbers in fp32, read off the sum with 2^23
+  const float p0 = fmaf(code[3], 4096.f, fmaf(code[2], 256.f, fmaf(code[1], 16.f, code[0] + 8388608.f)));
+  const float p1 = fmaf(code[7], 4096.f, fmaf(code[6], 256.f, fmaf(code[5], 16.f, code[4] + 8388608.f)));
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x5410);
+}
+__device__ __forceinline__ float kv4_reciprocal(float s) {
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  return inv;
+}
+
+// The smallest (low half) and minus the largest of this thread's eight channels.
+__device__ __forceinline__ uint32_t kv4_extremes(const uint4 raw) {
   const uint32_t mn = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
   const uint32_t mx = max_bf16x2(max_bf16x2(raw.x, raw.y), max_bf16x2(raw.z, raw.w));
-  // the smallest and minus the largest of the eight, then of the group
-  uint32_t both = min_bf16x2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
-  both = (both & 0xFFFFu) | ((max_bf16x2(mx, mx >> 16) << 16) ^ 0x80000000u);
+  const uint32_t both = min_bf16x2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+  return (both & 0xFFFFu) | ((max_bf16x2(mx, mx >> 16) << 16) ^ 0x80000000u);
+}
+
+// The codes of this thread's eight channels (as floats and packed), and the group's scale (bits 0 .. 15) and minimum.
+// The four threads of a group are lanes differing in bits 0 and 1.  both: kv4_extremes.
+__device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t both, uint32_t& scale, float (&code)[8]) {
   both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 1));
   both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, 2));
   float lo = __uint_as_float(both << 16), hi = -__uint_as_float(both & 0xFFFF0000u);
@@ -105,7 +146,6 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scal
   for (int i = 0; i < 8; ++i) code[i] = 0.f;
   if (!(lo >= -FLT_MAX && hi <= FLT_MAX)) {  // a NaN or an infinity
     scale = 0x7FC07FC0u;
-    code[0] = code[1] = code[2] = code[3] = code[4] = code[5] = code[6] = code[7] = 0.f;
     return 0u;
   }
   // Differences of values near the largest float would overflow: work 2^-16 smaller there.
@@ -118,29 +158,34 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4 raw, uint32_t& scal
   // and the reciprocal of a tiny scale would: work 2^64 larger there (both factors are exact)
   const float f = big < 0x1p-60f ? 0x1p64f : down;
   const float s = bf16_bits_to_float(scale_bits) * f;
-  lo *= f;
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  float x[8], t[8], far = 0.f;
+  float x[8];
   bf16x8_to_f32(raw, x);
-  const bool other = f != 1.f;
-  constexpr float ROUND = 12582912.f;  // 1.5 2^23: adding it rounds to a whole number, halves to even
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (other) x[i] *= f;
-    t[i] = (x[i] - lo) * inv;  // within 1e-5 of the quotient
-    code[i] = (t[i] + ROUND) - ROUND;
-    far = fmaxf(far, fabsf(t[i] - code[i]));
-  }
-  if (far > 0.49998f) {  // one of them is near a half
+  for (int i = 0; i < 8; ++i) x[i] *= f;
+  return kv4_codes(x, lo * f, s, kv4_reciprocal(s), code);
+}
+
+// The scales of four rows at once where no group of the warp is out of the ordinary (a NaN, an infinity, all values
+// equal, numbers that the above moves to another range): each of a group's four threads works one row's out, and all get
+// them by shuffles.  Returns whether that holds.
+__device__ __forceinline__ bool kv4_scales(const uint32_t (&both)[4], int lane, uint32_t (&scale)[4], float (&inv)[4]) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  uint32_t k0 = b1 ? both[2] : both[0], k1 = b1 ? both[3] : both[1];
+  k0 = min_bf16x2(k0, __shfl_xor_sync(0xffffffffu, b1 ? both[0] : both[2], 2));
+  k1 = min_bf16x2(k1, __shfl_xor_sync(0xffffffffu, b1 ? both[1] : both[3], 2));
+  const uint32_t mine = min_bf16x2(b0 ? k1 : k0, __shfl_xor_sync(0xffffffffu, b0 ? k0 : k1, 1));
+  const float lo = __uint_as_float(mine << 16), hi = -__uint_as_float(mine & 0xFFFF0000u);
+  const float big = fmaxf(fabsf(lo), fabsf(hi));
+  const bool plain = lo < hi && big <= 0x1p120f && big >= 0x1p-60f;  // false for NaN
+  if (!__all_sync(0xffffffffu, plain)) return false;
+  const uint32_t bits = kv4_scale_bits(lo, hi);
+  const float r = kv4_reciprocal(bf16_bits_to_float(bits));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (fabsf(t[i] - code[i]) > 0.49998f) code[i] = kv4_code_exact(x[i], lo, s, code[i]);
+  for (int u = 0; u < 4; ++u) {
+    scale[u] = __shfl_sync(0xffffffffu, bits | (mine << 16), u, 4);
+    inv[u] = __shfl_sync(0xffffffffu, r, u, 4);
   }
-  // 16-bit pieces as whole numbers in fp32, read off the sum with 2^23
-  const float p0 = fmaf(code[3], 4096.f, fmaf(code[2], 256.f, fmaf(code[1], 16.f, code[0] + 8388608.f)));
-  const float p1 = fmaf(code[7], 4096.f, fmaf(code[6], 256.f, fmaf(code[5], 16.f, code[4] + 8388608.f)));
-  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x5410);
+  return true;
 }
 
 // A thread's eight codes are the 16-bit pieces r = 2 t (low half) and 2 t + 1 (high half) of its group; the
@@ -167,7 +212,10 @@ __device__ __forceinline__ uint4 kv4_values(const float (&code)[8], uint32_t sca
   const float s = __uint_as_float(scale << 16), m = __uint_as_float(scale & 0xFFFF0000u);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = sm100::pack_bf16x2(fmaf(s, code[2 * i], m), fmaf(s, code[2 * i + 1], m));
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = sm100::ffma2(make_float2(code[2 * i], code[2 * i + 1]), make_float2(s, s), make_float2(m, m));
+    w[i] = sm100::pack_bf16x2(x.x, x.y);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // Eight packed codes as floats: two at a time as fp16 1024 + c, which is exact.
@@ -211,16 +259,35 @@ __device__ __forceinline__ void kv4_move(const Place& place, bool want_read, int
   } else {
     uint4 raw[KV4_UNROLL];
 #pragma unroll
-    for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = place.on(u) ? ld_nc_v4(place.row(u)) : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < KV4_UNROLL; ++u) raw[u] = place.on(u) ? ld_nc_v4(place.row(u)) : make_uint4(0x3F800000u, 0, 0, 0);  // an ordinary row
+    static_assert(KV4_UNROLL == 4, "a row for each of a group's four threads");
+    uint32_t both[KV4_UNROLL], scales[KV4_UNROLL];
+    float inv[KV4_UNROLL];
 #pragma unroll
-    for (int u = 0; u < KV4_UNROLL; ++u) {
-      uint32_t scale;
-      float code[8];
-      const uint32_t word = kv4_to_words<NG>(kv4_quantise(raw[u], scale, code), lane);
+    for (int u = 0; u < KV4_UNROLL; ++u) both[u] = kv4_extremes(raw[u]);
+    auto put = [&](int u, uint32_t codes, uint32_t scale, const float (&code)[8]) {
+      const uint32_t word = kv4_to_words<NG>(codes, lane);
       if (place.on(u)) {
         *place.codes(u) = word;
         if (first_of_group) *place.scales(u) = scale;
         if (want_read) *place.read(u) = kv4_values(code, scale);
+      }
+    };
+    float code[8];
+    if (kv4_scales(both, lane, scales, inv)) {
+#pragma unroll
+      for (int u = 0; u < KV4_UNROLL; ++u) {
+        float x[8];
+        bf16x8_to_f32(raw[u], x);
+        put(u, kv4_codes(x, __uint_as_float(scales[u] & 0xFFFF0000u), bf16_bits_to_float(scales[u] & 0xFFFFu), inv[u], code),
+            scales[u], code);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < KV4_UNROLL; ++u) {
+        uint32_t scale;
+        const uint32_t codes = kv4_quantise(raw[u], both[u], scale, code);
+        put(u, codes, scale, code);
       }
     }
   }
