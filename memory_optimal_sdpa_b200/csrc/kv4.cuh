@@ -7,7 +7,8 @@
 // Both directions are streams (append: 2 d bytes in and d / 2 + d / 8 out per row, plus 2 d for the values
 // read back; load: the reverse), so a thread moves 16 bytes of bf16 with one access: eight channels
 // 32 g + 8 t .. + 7 (t = 0 .. 3), which are the pieces r = 2 t and 2 t + 1 of group g.  The four threads
-// of a group find its extremes by two shuffles.
+// of a group find its extremes by shuffles.  Load runs at HBM's rate; append is bound by its instructions (about 150 per eight
+// channels of 32 threads), then HBM: 4.85 TB/s for 250 MB.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -229,7 +230,11 @@ __device__ __forceinline__ void kv4_unpack(uint32_t codes, float (&code)[8]) {
   }
 }
 
-constexpr int KV4_THREADS = 256;
+// Blocks of 128 threads at 64 registers.  4 x 8 heads, d = 128: append of 5001-8192 rows 51.7 us, load of 9001-16384 rows 45.3 us;
+// 256 threads at 78 registers 57.2 and 47.0 us, at 64 registers 51.8 and 46.9 us, 128 threads at 72 and 56 registers 53.0
+// and 51.1 us (append), 64 threads 51.5 and 46.3 us.
+constexpr int KV4_THREADS = 128;
+constexpr int KV4_BLOCKS = 8;  // per SM
 constexpr int KV4_UNROLL = 4;  // rows a thread has in flight
 
 // Length of sequence b clamped to [0, n_cap]; anything else is recorded.
@@ -297,7 +302,7 @@ __device__ __forceinline__ void kv4_move(const Place& place, bool want_read, int
 // sequence and head (every block of a long prompt) knows its places as one base and fixed offsets, and leaves at once where no
 // row is to be moved; the others (single tokens) find each row's place by itself.
 template <int D, bool LOAD>
-__global__ void __launch_bounds__(KV4_THREADS) sdpa_kv4_rows_kernel(const Kv4RowsParams p) {
+__global__ void __launch_bounds__(KV4_THREADS, KV4_BLOCKS) sdpa_kv4_rows_kernel(const Kv4RowsParams p) {
   constexpr int NG = D / 32, TPR = D / 8;  // threads per row
   constexpr int RPB = KV4_THREADS / TPR;   // rows per block and pass
   const int lane = threadIdx.x & 31;
