@@ -10,10 +10,10 @@
 // A unit of work is 128 MT keys of one (sequence, key/value head); its queries stream past in tiles of 128, head
 // after head.  MT = 2 halves the waits of the producer and the MMA issuer and the L2 traffic of the queries; MT = 1 is
 // for fewer than 148 units of 256 keys.  Measured, MT = 2 against 1: 32 heads over 8, n = 8192, causal 352 and 369 us; the last 64
-// queries of 4 x 16 heads, 16001 keys, d = 64 45 and 57 us.  What bounds it: for many queries the exponentials (16
+// queries of 4 x 16 heads, 16001 keys, d = 64 45 and 57 us when this was chosen (44 us now).  What bounds it: for many queries the exponentials (16
 // per clock and SM on the MUFU unit, so 1024 clocks for 128 x 128 scores, against 512 for the MMA at d = 128; 239 us for the
 // former case, whose heaviest unit is also 12 % above an SM's share).  For few queries the hand-offs of a
-// unit (about 1900 clocks in the MMA issuer), not HBM (21 us for the latter case).
+// unit and its exponentials in a chain (about 3000 clocks for 256 keys and 64 queries), not HBM (21 us for the latter case).
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 and 3 log-sum-exps into shared memory, then softmax groups of
 // four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
@@ -288,6 +288,10 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         const int row = 128 * x.qt + 32 * i + lane;
         v[i] = row < p.n_q ? __ldg(L + row) : -__int_as_float(0x7f800000);
       }
+      // A new unit: its keys' weights on the way to L2, for the groups to add to (loaded at the unit's start instead they took
+      // a register too many and their latency: 47.4 us against 43.9 for the last 64 queries above).
+      if (p.acc && x.h == 0 && x.qt == x.g.qt0 && lane < 4 * MT && x.g.key0 + 32 * lane < p.n_kv)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.acc + (size_t)x.g.bkv * p.n_acc + x.g.key0 + 32 * lane));
     };
     Walk x;
     bool more = begin(x.g);
@@ -310,10 +314,11 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         const float y = -1.4426950408889634f * v[i];
         // a query that sees no key (LSE -inf) or does not exist adds nothing
         sL[st * 128 + 32 * i + lane] = y == __int_as_float(0x7f800000) ? -y : y;
-        v[i] = next_v[i];
       }
       __syncwarp();
       if (lane < MT) mbar_arrive(&s_full[st * MT + lane]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = next_v[i];  // after the arrival: it waits for them
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax groups
@@ -330,7 +335,6 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       const int key = g.key0 + 32 * kw + lane;
       const int warp_last = g.key0 + 32 * kw + 31;  // the warp's last key: masks the most
       const size_t at = (size_t)g.bkv * p.n_acc + key;
-      const float before = p.acc && key < p.n_kv ? p.acc[at] : 0.f;  // early: its latency is a unit's work away
       float w = 0.f;
       const int skip = (turn - nq % C::TURNS + C::TURNS) % C::TURNS;  // this turn's first tile of the unit
       int qt = g.qt0 + (tiles_head ? skip % tiles_head : 0);
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
       }
       nq += tiles;
       if (!ok || turn != last_turn) continue;
-      if (key < p.n_kv) p.acc_out[at] = before + w;
+      if (key < p.n_kv) p.acc_out[at] = (p.acc ? p.acc[at] : 0.f) + w;
     }
   }
 
