@@ -299,7 +299,7 @@ struct CacheQuery {
         // largest element in [2^14, 2^15); a zero row keeps its (irrelevant) factor
         const int e = (int)(__float_as_uint(big) >> 23) - 127;
         const float up = exp2_int((14 - e) / 2), up2 = exp2_int(14 - e - (14 - e) / 2);  // two exact steps: 2^(14 - e) itself may overflow
-        norm[x] = exp2_int(min(e, 126) - 2);
+        norm[x] = exp2_int(min(e, 127) - 2);
         if (e < -124) norm[x] = 0x1p-126f * exp2_int(e + 124);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {

@@ -1,0 +1,98 @@
+"""Decodes over the bounded cache at the ends of their range: queries, scales and rows of any finite size, and rows of values of unlike size.
+
+Each result is held against 64 bits within what its roundings add up to.  A score is a sum of d products that the tensor cores
+take 16 at a time: counted as one unit, 2^-23 of |q|_2 |k|_2 |scale|, per step and eight for what comes after, it is off by at
+most delta = (d / 16 + 8) 2^-23 |q|_2 |k|_2 |scale|.  The LSE is off by the mean of its keys' deltas by weight, and by
+2^-20 (1 + |LSE|) for its own exponentials and logarithm; a weight exp(score - LSE) by a factor 1 +- rel, rel the sum of both.
+A weight enters the sum of values rounded to 12 bits with its row's scale (4-bit caches) or as two bf16 parts (16 bits), and
+the output is rounded to bf16 (half a step: 2^-8).
+"""
+import pytest
+from test_cache_gpu import i32, random_cache, rnd, values64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sdpa(cuda_device):
+    import memory_optimal_sdpa_b200 as m
+    yield m
+    assert m.get_last_device_error() == m.SDPA_OK
+
+
+def values_abs64(codes, scales):
+    """s c + |m|: what the products of a 4-bit row add up to before signs cancel."""
+    s = scales.clone()
+    s[..., 1] = s[..., 1].abs()
+    return values64(codes, s)
+
+
+def check(sdpa, q, cache, lens, scale, acc=None):
+    """One decode over `cache` (4-bit, or a pair of bf16 tensors) against 64 bits, head by head."""
+    import torch
+    bits4 = len(cache) == 4
+    if bits4:
+        k, v = values64(cache[0], cache[1]), values64(cache[2], cache[3])
+        k_abs, v_abs = values_abs64(cache[0], cache[1]), values_abs64(cache[2], cache[3])
+    else:
+        k, v = cache[0].double(), cache[1].double()
+        k_abs, v_abs = k.abs(), v.abs()
+    B, Hkv, cap, d = k.shape
+    G = q.shape[1] // Hkv
+    acc = torch.zeros((B, Hkv, cap), device="cuda") if acc is None else acc
+    call = sdpa.decode_kv4(q, sdpa.Kv4Cache(*cache), i32(lens), scale=scale, acc=acc) if bits4 else sdpa.decode_acc(q, *cache, i32(lens), acc, scale=scale)
+    O, L = (t.double().view(B, Hkv, G, -1) for t in call)
+    for b, n in enumerate(lens):
+        for h in range(Hkv):
+            qq = q[b].double().view(Hkv, G, d)[h]
+            s = qq @ k[b, h, :n].T * scale
+            lse = torch.logsumexp(s, -1)
+            p = torch.softmax(s, -1)
+            # per key; the LSE is off by what its keys' scores are, weighted
+            delta = (d / 16 + 8) * 2.0 ** -23 * qq.norm(dim=-1)[:, None] * k_abs[b, h, :n].norm(dim=-1) * abs(scale)
+            of_lse = (p * delta).sum(-1, keepdim=True) + 2.0 ** -20 * (1 + lse[:, None].abs())
+            rel = delta + of_lse
+            assert (p * rel).sum(-1).max() < 0.02  # the inputs leave something to check
+            assert ((L[b, h] - lse[:, None]).abs() <= of_lse).all(), (b, h)
+            want = p @ v[b, h, :n]
+            allowed = 2.0 ** -8 * want.abs() + (p * ((2.0 ** -12 if bits4 else 2.0 ** -17) + rel)) @ v_abs[b, h, :n] + 2.0 ** -126
+            assert ((O[b, h] - want).abs() <= allowed).all(), (b, h, ((O[b, h] - want).abs() / allowed).max().item())
+            # a weight below 2^-126 is not a normal 32-bit number
+            assert ((acc[b, h, :n].double() - p.sum(0)).abs() <= (rel * p).sum(0) + 2.0 ** -22 * p.sum(0) + G * 2.0 ** -126).all()
+
+
+def scaled(cache, which, factor):
+    """A cache whose keys or values are `factor` (a power of two) times as large."""
+    cache = list(cache)
+    at = {"k": 0, "v": 1}[which]
+    at = 2 * at + 1 if len(cache) == 4 else at
+    cache[at] = (cache[at].double() * factor).to(cache[at].dtype)
+    return cache
+
+
+def make(sdpa, bits, B, Hkv, cap, d, lens, seed):
+    if bits == 4:
+        return list(random_cache(sdpa, B, Hkv, cap, d, lens, seed))
+    return [rnd((B, Hkv, cap, d), seed), rnd((B, Hkv, cap, d), seed + 1)]
+
+
+# ------------------------------------------------------------------------------------------ sizes of q, of the scale and of the keys
+# The largest element of a head is in [2^e, 2^(e + 1)), scale is 2^a / 8, keys are times 2^b; e + a + b = 0 but for the last.
+EXPONENTS = [(127, -124, 0), (126, -123, 0), (125, -125, 0), (124, -124, 0), (60, -60, 0), (-60, 60, 0), (127, -127, -3)]
+
+
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 12)])
+@pytest.mark.parametrize("e,a,b", EXPONENTS)
+@pytest.mark.parametrize("bits", [4, 16])
+def test_size_of_queries_scale_and_keys(sdpa, bits, e, a, b, d, G):
+    import torch
+    q = rnd((1, G, d), 1).double()
+    if bits == 16 and e + b > 115:
+        pytest.skip("the product q k is beyond 32 bits")
+    top = q.abs().amax(-1, keepdim=True)
+    q = (q / top * 1.5 * 2.0 ** e).to(torch.bfloat16)
+    cache = scaled(make(sdpa, bits, 1, 1, 150, d, [150], 2), "k", 2.0 ** b)
+    scale = 2.0 ** a / 8
+    assert torch.isfinite(q).all()
+    check(sdpa, q, cache, [150], scale)
+    check(sdpa, q, cache, [150], -scale)
