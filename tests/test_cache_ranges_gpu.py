@@ -78,7 +78,8 @@ def make(sdpa, bits, B, Hkv, cap, d, lens, seed):
 
 # ------------------------------------------------------------------------------------------ sizes of q, of the scale and of the keys
 # The largest element of a head is in [2^e, 2^(e + 1)), scale is 2^a / 8, keys are times 2^b; e + a + b = 0 but for the last.
-EXPONENTS = [(127, -124, 0), (126, -123, 0), (125, -125, 0), (124, -124, 0), (60, -60, 0), (-60, 60, 0), (127, -127, -3)]
+EXPONENTS = [(127, -124, 0), (126, -123, 0), (125, -125, 0), (120, 0, -120), (127, -7, -120), (110, 10, -120), (124, -124, 0), (60, -60, 0),
+             (-60, 60, 0), (-100, 100, 0), (-120, 120, 0), (-126, 126, 0), (-126, 66, 60), (-20, -100, 120), (-126, 6, 120), (127, -127, -3)]
 
 
 @pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 12)])
@@ -96,3 +97,33 @@ def test_size_of_queries_scale_and_keys(sdpa, bits, e, a, b, d, G):
     assert torch.isfinite(q).all()
     check(sdpa, q, cache, [150], scale)
     check(sdpa, q, cache, [150], -scale)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_heads_of_unlike_size(sdpa, bits):
+    """Each head has a factor of its own; one with a score that counts beside others that are far from it."""
+    import torch
+    d, sizes = 64, [127, 120, 100, 3, 0, -20, -126, 125] if bits == 4 else [115, 108, 88, 3, 0, -20, -126, 113]
+    q = rnd((1, 8, d), 1).double()
+    q = (q / q.abs().amax(-1, keepdim=True) * 1.5 * 2.0 ** torch.tensor(sizes, device="cuda")[:, None].double()).to(torch.bfloat16)
+    check(sdpa, q, make(sdpa, bits, 1, 1, 97, d, [97], 2), [97], 2.0 ** -max(sizes))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127])
+@pytest.mark.parametrize("bits", [4, 16])
+def test_largest_scales(sdpa, bits, scale):
+    """Scores of 0 are 0, and small ones are what they are."""
+    import torch
+    d, n = 64, 100
+    q, k = torch.zeros((1, 2, d), device="cuda"), torch.zeros((1, 1, n, d), device="cuda")
+    q[0, 0, 5], q[0, 1, 37] = 2.0 ** -63, -(2.0 ** -62)
+    k[..., 5], k[..., 37] = 2.0 ** -63 * (torch.arange(n) % 7 - 3), 2.0 ** -63 * (torch.arange(n) % 3)
+    v = rnd((1, 1, n, d), 3)
+    q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+    if bits == 4:
+        cache = sdpa.kv4_cache(1, 1, n, d)
+        sdpa.kv4_append(cache, k, v, i32([0]))
+        # the groups' codes give these keys back exactly, or nearly: what the cache stands for counts
+        check(sdpa, q, list(cache), [n], scale)
+    else:
+        check(sdpa, q, [k, v], [n], scale)
