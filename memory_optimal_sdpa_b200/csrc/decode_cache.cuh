@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
       // |scale log2 e| 2^exp in two steps, which leave the range only where the result does.  Beyond 2^126 the scores are first
-      // multiplied by 2^126 (`far`; at most 1 % slower for testing it).  Not 0 (scale 0), which would make NaN of the -inf of a key past the length:
-      // 2^-126 leaves every other weight 1.
+      // multiplied by 2^126 (`far`; at most 1 % slower for testing it).  Not 0 (scale 0), which would make NaN of the -inf
+      // of a key past the length: with the smallest float, 2^-149, no score that is finite before comes to 2^-20.
       const float c = fabsf(p.scale_log2);
       const int e = __shfl_sync(0xffffffffu, q.exp[x], 8 * t + 4 * y);
       c2[x][y] = c * exp2_int(e / 2) * exp2_int(e - e / 2);
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         far |= 1u << (2 * x + y);
         c2[x][y] = fminf(c * exp2_int((e - 126) / 2) * exp2_int(e - 126 - (e - 126) / 2), FLT_MAX);
       }
-      c2[x][y] = fmaxf(c2[x][y], FLT_MIN);
+      c2[x][y] = fmaxf(c2[x][y], 0x1p-149f);
     }
 
   // Tiles whose scores need no second look: not the one that the length ends in, none where a column is far.

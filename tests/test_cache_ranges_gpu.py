@@ -127,3 +127,14 @@ def test_largest_scales(sdpa, bits, scale):
         check(sdpa, q, list(cache), [n], scale)
     else:
         check(sdpa, q, [k, v], [n], scale)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, -(2.0 ** -140)])
+def test_scale_of_nothing_with_huge_keys(sdpa, bits, scale):
+    """A scale of 0 (or next to it) gives every key the same weight, however large its products are."""
+    import torch
+    d, n = 64, 80
+    cache = scaled(make(sdpa, bits, 1, 1, n, d, [n], 5), "k", 2.0 ** 100)
+    q = (rnd((1, 3, d), 6).double() * 2.0 ** 17).to(torch.bfloat16)
+    check(sdpa, q, cache, [n], scale)
