@@ -65,7 +65,8 @@ struct CacheDecodeParams {
   int block;         // keys per block of work
   int n_cta;
   int score_stride;  // n_cap rounded up to 4
-  float scale_log2;
+  float scale_log2;  // scale log2 e, or a quarter of it
+  int scale_exp;     // 2 where it is a quarter: log2 e takes the largest scales out of range
 };
 
 // WIDE: 9 to 16 query heads per CTA, else up to 8.  The MMA has 16 rows either way.
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   q.load(p.Q + head0 * D, heads, p.scale_log2 < 0.f ? 0x80008000u : 0u, lane);
   // A thread's columns are the heads 8 x + 2 t + y (y = 0, 1).
   float c2[NR][2];
-  uint32_t far = 0;  // 4-bit: a bit per column
+  uint32_t far = 0;  // a bit per column
 #pragma unroll
   for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -451,9 +452,9 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
       // multiplied by 2^126 (`far`; at most 1 % slower for testing it).  Not 0 (scale 0), which would make NaN of the -inf
       // of a key past the length: with the smallest float, 2^-149, no score that is finite before comes to 2^-20.
       const float c = fabsf(p.scale_log2);
-      const int e = __shfl_sync(0xffffffffu, q.exp[x], 8 * t + 4 * y);
+      const int e = __shfl_sync(0xffffffffu, q.exp[x], 8 * t + 4 * y) + p.scale_exp;
       c2[x][y] = c * exp2_int(e / 2) * exp2_int(e - e / 2);
-      if (KV4 && c2[x][y] > 0x1p126f) {
+      if (c2[x][y] > 0x1p126f) {
         far |= 1u << (2 * x + y);
         c2[x][y] = fminf(c * exp2_int((e - 126) / 2) * exp2_int(e - 126 - (e - 126) / 2), FLT_MAX);
       }
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     }
 
   // Tiles whose scores need no second look: not the one that the length ends in, none where a column is far.
-  const int plain_tiles = KV4 && __any_sync(0xffffffffu, far != 0) ? 0 : n / C::TILE;
+  const int plain_tiles = __any_sync(0xffffffffu, far != 0) ? 0 : n / C::TILE;
 
   // Outputs, transposed: rows are channels (4-bit: tile 2 g + h holds channels 32 g + 4 r + 2 h and, in rows 8 .. 15, + 1;
   // bf16: 16 c + r and + 8), columns heads.  om: sums of p m.
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
       }
     }
     if (tile >= plain_tiles) {
-      if (KV4 && far) {
+      if (far) {
 #pragma unroll
         for (int x = 0; x < NR; ++x)
 #pragma unroll

@@ -109,10 +109,10 @@ def test_heads_of_unlike_size(sdpa, bits):
     check(sdpa, q, make(sdpa, bits, 1, 1, 97, d, [97], 2), [97], 2.0 ** -max(sizes))
 
 
-@pytest.mark.parametrize("scale", [2.0 ** 127])
+@pytest.mark.parametrize("scale", [2.0 ** 127, 1.4765625 * 2.0 ** 127, (2 - 2.0 ** -23) * 2.0 ** 127, -(2 - 2.0 ** -23) * 2.0 ** 127])
 @pytest.mark.parametrize("bits", [4, 16])
 def test_largest_scales(sdpa, bits, scale):
-    """Scores of 0 are 0, and small ones are what they are."""
+    """scale log2 e may be beyond the largest 32-bit number: scores of 0 are 0, and small ones are what they are."""
     import torch
     d, n = 64, 100
     q, k = torch.zeros((1, 2, d), device="cuda"), torch.zeros((1, 1, n, d), device="cuda")
