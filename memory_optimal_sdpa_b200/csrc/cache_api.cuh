@@ -340,7 +340,8 @@ extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, cons
   p.n_acc = n_acc;
   p.causal = causal;
   p.bkv = batch * heads_kv;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.quarter = std::fabs(scale) > 0x1p126f;
+  p.scale_log2 = (p.quarter ? 0.25f * scale : scale) * 1.4426950408889634f;
   cudaStream_t s = (cudaStream_t)stream;
   const bool wide = prompt_wide(p);
   if (d == 64) return wide ? launch_prompt_weights<64, 2>(Q, K, p, batch, s) : launch_prompt_weights<64, 1>(Q, K, p, batch, s);

@@ -33,7 +33,8 @@ struct PromptWeightsParams {
   float* acc_out;
   int heads_q, heads_kv, group, n_q, n_kv, n_acc, causal;
   int bkv, n_kt;           // B Hkv; key units per (sequence, key/value head)
-  float scale_log2;
+  float scale_log2;        // scale log2 e, or a quarter of it
+  int quarter;             // log2 e takes the largest scales out of range: their products are multiplied by 4 first
 };
 
 template <int D, int MT>
@@ -354,7 +355,8 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
         float2 part = make_float2(0.f, 0.f);
         uint32_t s[2][16];
         tmem_ld_32x32b_x16(ta, s[0]);
-        if (!masked && cols == 128) {
+        const int plain = masked || p.quarter ? 0 : cols;  // columns that are just added up
+        if (plain == 128) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             tmem_wait_ld();
@@ -370,10 +372,14 @@ __global__ void __launch_bounds__(PromptCfg<D, MT>::THREADS, 1)
               tmem_wait_ld();
               reg_fence(s[y]);
               if (c + y < 7) tmem_ld_32x32b_x16(ta + (uint32_t)(16 * (c + y + 1)), s[y ^ 1]);
-              if (!masked && 16 * (c + y + 1) <= cols)
+              if (16 * (c + y + 1) <= plain) {
                 part = prompt_chunk<false>(s[y], c2, L + 4 * (c + y), 0, 16, part);
-              else
-                part = prompt_chunk<true>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), cols - 16 * (c + y), part);
+                continue;
+              }
+              if (p.quarter)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[y][i] = __float_as_uint(4.f * __uint_as_float(s[y][i]));
+              part = prompt_chunk<true>(s[y], c2, L + 4 * (c + y), first - 16 * (c + y), cols - 16 * (c + y), part);
             }
           tmem_wait_ld();  // the load ahead of the last columns
         }

@@ -138,3 +138,23 @@ def test_scale_of_nothing_with_huge_keys(sdpa, bits, scale):
     cache = scaled(make(sdpa, bits, 1, 1, n, d, [n], 5), "k", 2.0 ** 100)
     q = (rnd((1, 3, d), 6).double() * 2.0 ** 17).to(torch.bfloat16)
     check(sdpa, q, cache, [n], scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q,n_kv,causal", [(128, 256, False), (300, 300, True), (5, 64, True)])
+@pytest.mark.parametrize("scale", [2.0 ** 126, (2 - 2.0 ** -23) * 2.0 ** 127, -(2 - 2.0 ** -23) * 2.0 ** 127])
+def test_prompt_weights_of_the_largest_scales(sdpa, scale, n_q, n_kv, causal, d):
+    import torch
+    q, k = torch.zeros((1, 2, n_q, d), device="cuda"), torch.zeros((1, 1, n_kv, d), device="cuda")
+    q[0, 0, :, 5], q[0, 1, :, 37] = 2.0 ** -63 * (torch.arange(n_q) % 3), -(2.0 ** -62)
+    k[..., 5], k[..., 37] = 2.0 ** -63 * (torch.arange(n_kv) % 7 - 3), 2.0 ** -63 * (torch.arange(n_kv) % 3)
+    q, k = q.to(torch.bfloat16), k.to(torch.bfloat16)
+    s = q.double() @ k.double().transpose(-1, -2) * scale
+    if causal:
+        s.masked_fill_(torch.arange(n_kv, device="cuda") > torch.arange(n_q, device="cuda")[:, None] + (n_kv - n_q), -torch.inf)
+    lse = torch.logsumexp(s, -1).float()
+    want = torch.exp(s - lse[..., None].double()).sum((1, 2))
+    acc = sdpa.fwd_acc(q, k, lse, causal=causal, scale=scale)
+    # products of powers of two with one to three, exact; the exponents round at 2^-24 of |score| + |LSE| < 32, and the sums as in other cases
+    rel = 32 * 2.0 ** -23 + 2.0 ** -18 + 2.0 ** -22 * (2 * n_q) ** 0.5
+    assert ((acc.double()[:, 0] - want).abs() <= rel * want + 2 * n_q * 2.0 ** -126).all()
