@@ -774,9 +774,11 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         float M = NEG_INF, L = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, s_stat[w][row].x);
+        // no key scores more than -inf: 0 and -inf, as without a key (L is 0, or NaN where a score is)
+        if (M == NEG_INF) M = 0.f;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) L = fmaf(sm100::ex2_approx(s_stat[w][row].x - M), s_stat[w][row].y, L);
-        const float mul = sm100::ex2_approx(m_ref[x][y] - M) / L;  // of this warp's sums
+        const float mul = L == 0.f ? 0.f : sm100::ex2_approx(m_ref[x][y] - M) / L;  // of this warp's sums
         if (warp == 0 && r == 0 && row < heads) {
           const float l2 = M + log2f(L);
           p.part_lse[part0 + row] = l2;
@@ -878,11 +880,11 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     const int row = warp % p.rows, set = warp / p.rows, sets = WARPS / p.rows;
     float acc[E] = {};
     if (row < heads) {
-      const float l2 = row_lse(g, row);
+      const float l2 = row_lse(g, row), off = l2 == NEG_INF ? 0.f : l2;  // all parts -inf: 2^-inf
 #pragma unroll 4
       for (int s = set; s < g.n; s += sets) {
         const size_t part = (g.first + s) * p.rows + row;
-        const float w = exp2f(p.part_lse[part] - l2);
+        const float w = exp2f(p.part_lse[part] - off);
         const float* v = p.part_o + part * D + lane * E;
         if constexpr (E == 4) {
           const float4 u = *reinterpret_cast<const float4*>(v);
@@ -911,7 +913,7 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     if (h0) __syncthreads();
     if (warp < nh) {
       const float x = row_lse(segments((h0 + warp) / p.rows), (h0 + warp) % p.rows);
-      if (lane == 0) s_lse[warp] = x;
+      if (lane == 0) s_lse[warp] = x == NEG_INF ? 0.f : x;  // its scores are all -inf: weights of 0
     }
     __syncthreads();
 #pragma unroll

@@ -7,6 +7,8 @@ most delta = (d / 16 + 8) 2^-23 |q|_2 |k|_2 |scale|.  The LSE is off by the mean
 A weight enters the sum of values rounded to 12 bits with its row's scale (4-bit caches) or as two bf16 parts (16 bits), and
 the output is rounded to bf16 (half a step: 2^-8).
 """
+import math
+
 import pytest
 from test_cache_gpu import i32, random_cache, rnd, values64
 
@@ -158,3 +160,37 @@ def test_prompt_weights_of_the_largest_scales(sdpa, scale, n_q, n_kv, causal, d)
     # products of powers of two with one to three, exact; the exponents round at 2^-24 of |score| + |LSE| < 32, and the sums as in other cases
     rel = 32 * 2.0 ** -23 + 2.0 ** -18 + 2.0 ** -22 * (2 * n_q) ** 0.5
     assert ((acc.double()[:, 0] - want).abs() <= rel * want + 2 * n_q * 2.0 ** -126).all()
+
+
+# ------------------------------------------------------------------------------------------ keys that count nothing
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 12])
+@pytest.mark.parametrize("lo,hi", [(0, 64), (0, 200), (64, 128), (100, 300), (0, 700), (640, 700), (0, 699), (1, 700)])
+def test_keys_of_minus_infinity(sdpa, d, G, lo, hi):
+    """Keys lo .. hi - 1 score -inf with every head of a group: they weigh 0, and nothing else changes.  Where they are all the keys
+    there are, O = 0, LSE = -inf and every weight is 0, as for a sequence of length 0."""
+    import torch
+    n, Hkv = 700, 2
+    q, k, v = rnd((2, Hkv * G, d), 1), rnd((2, Hkv, n + 3, d), 2), rnd((2, Hkv, n + 3, d), 3)
+    q[..., 5] = q[..., 5].abs() + 0.5
+    k[0, 1, lo:hi, 5] = -math.inf
+    acc = torch.zeros((2, Hkv, n + 3), device="cuda")
+    O, L = sdpa.decode_acc(q, k, v, i32([n, n]), acc)
+    rest = [j for j in range(n) if not lo <= j < hi]
+    assert torch.isfinite(O).all() and (acc[0, 1, lo:hi] == 0).all()
+    if rest:
+        short = torch.zeros((1, 1, len(rest)), device="cuda")
+        heads = slice(G, 2 * G)
+        o, l = sdpa.decode_acc(q[:1, heads].contiguous(), k[:1, 1:, rest].contiguous(), v[:1, 1:, rest].contiguous(), i32([len(rest)]), short)
+        # the same keys in another order of summation
+        assert torch.allclose(O[:1, heads].float(), o.float(), rtol=2.0 ** -6, atol=2.0 ** -10) and torch.allclose(L[:1, heads], l, rtol=0, atol=1e-4)
+        assert torch.allclose(acc[0, 1, rest], short[0, 0], rtol=2e-4, atol=0)
+    else:
+        assert (O[0, G:] == 0).all() and (L[0, G:] == -math.inf).all()
+    plain = torch.zeros_like(acc)
+    k[0, 1, lo:hi, 5] = 0
+    O2, L2 = sdpa.decode_acc(q, k, v, i32([n, n]), plain)
+    others = [(0, 0), (1, 0), (1, 1)]
+    for b, h in others:
+        at = slice(h * G, h * G + G)
+        assert torch.equal(O[b, at], O2[b, at]) and torch.equal(L[b, at], L2[b, at]) and torch.equal(acc[b, h], plain[b, h])
