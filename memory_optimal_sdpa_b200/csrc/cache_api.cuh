@@ -171,13 +171,13 @@ CacheParts cache_parts(long long batch, int heads_q, int heads_kv, int d, bool k
   return {rows, (units + cache_ctas(d, kv4, rows == 16)) * rows};
 }
 
-// Floats: d outputs and one log-sum-exp per row of the partial results (a multiple of 8 rows), and the scores per (head,
+// Floats: d outputs, a maximum and a sum per row of the partial results (a multiple of 8 rows), and the scores per (head,
 // cache row); then one 64-bit number per sequence and one more.
 size_t cache_ws_size(int batch, int heads_q, int heads_kv, int n_cap, int d, bool kv4, bool with_acc) {
   if (batch <= 0 || heads_q <= 0 || heads_kv <= 0 || heads_q % heads_kv != 0 || n_cap <= 0 || !cache_head_dim(d)) return 0;
   const CacheParts parts = cache_parts(batch, heads_q, heads_kv, d, kv4);
   const long long scores = with_acc ? (long long)batch * heads_q * cache_score_stride(n_cap) : 0;
-  return (size_t)(parts.rows * (d + 1) + scores) * sizeof(float) + (size_t)(batch + 2) / 2 * 2 * sizeof(long long);
+  return (size_t)(parts.rows * (d + 2) + scores) * sizeof(float) + (size_t)(batch + 2) / 2 * 2 * sizeof(long long);
 }
 
 template <int D, bool KV4, bool WIDE>
@@ -236,8 +236,8 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   p.scale_log2 = (p.scale_exp ? 0.25f * scale : scale) * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.scores = acc_out ? p.part_o + (size_t)parts.rows * d : nullptr;  // 16-byte rows: the stride is a multiple of 4
-  p.part_lse = p.part_o + (size_t)parts.rows * d + (acc_out ? (size_t)batch * heads_q * p.score_stride : 0);
-  p.seq_at = (long long*)(p.part_lse + parts.rows);
+  p.part_stat = (float2*)(p.part_o + (size_t)parts.rows * d + (acc_out ? (size_t)batch * heads_q * p.score_stride : 0));
+  p.seq_at = (long long*)(p.part_stat + parts.rows);
   cudaStream_t s = (cudaStream_t)stream;
   if (d == 64) return kv4 ? launch_cache_decode<64, true>(p, s) : launch_cache_decode<64, false>(p, s);
   return kv4 ? launch_cache_decode<128, true>(p, s) : launch_cache_decode<128, false>(p, s);

@@ -5,10 +5,10 @@
 // line of work that is cut evenly among as many CTAs as fit on the GPU at once: lengths differ, and a
 // wave that is not full costs as much as a full one (splits of 2048 keys 183 us, two, three, four lines' worth of CTAs 168,
 // 170, 173 us against 165 us for the case below).  A CTA's cut is one or more segments, each of one unit; a segment gives
-// a normalised partial output and a log-sum-exp (base 2) per query head.  Segment number unit + CTA is unique,
+// a normalised partial output and a log-sum-exp (base 2, as a maximum and a sum) per query head.  Segment number unit + CTA is unique,
 // as both only grow along the line.  With weights the scores (base 2, fp32) are written too: a key's weight
 // needs the log-sum-exp over all of its unit's segments, and 4 bytes a score, written and read once, cost far less than
-// reading the keys again.  sdpa_cache_finish_kernel joins the segments and adds sum_h 2^(score_h - LSE_h) per key.
+// reading the keys again.  sdpa_cache_finish_kernel joins the segments and adds sum_h 2^(score_h - m_h) / l_h per key.
 //
 // What bounds it: HBM, if the arithmetic fits under it.  A 4-bit row pair of d = 128 is 160 bytes, 6.9 clocks of an
 // SM's share of HBM, in which 256 codes have to become operands.  So the codes never leave registers:
@@ -52,7 +52,7 @@ struct CacheDecodeParams {
   Kv4Cache cache[2];            // or 4-bit cache K, V
   const int* kv_lens;
   float* part_o;    // [units + CTAs, ROWS, D]
-  float* part_lse;  // [units + CTAs, ROWS], base 2
+  float2* part_stat;  // [units + CTAs, ROWS]: a reference m (-inf: no key counts) and the sum of 2^(score - m), base 2
   long long* seq_at;  // [B + 1]: blocks of work before each sequence, and all of them
   float* scores;    // [B, Hq, score_stride], base 2, or null
   const float* acc;
@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   long long at = line.begin(cta);
   const long long end = line.begin(cta + 1);
   __shared__ float2 s_stat[C::WARPS][C::ROWS];  // m, l
+  __shared__ float s_pre[C::THREADS][2 * NR];   // each thread's own: see `far`
   if (cta == 0 && warp == 0) CacheLine::write(p, lane);
   int b = 0;
   long long seq_at = CacheLine::find(p, lane, at, b);  // where sequence b begins
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   q.load(p.Q + head0 * D, heads, p.scale_log2 < 0.f ? 0x80008000u : 0u, lane);
   // A thread's columns are the heads 8 x + 2 t + y (y = 0, 1).
   float c2[NR][2];
-  uint32_t far = 0;  // a bit per column
+  uint32_t far = 0;  // a bit per column; four bits up: scores multiplied by s_pre
 #pragma unroll
   for (int x = 0; x < NR; ++x)
 #pragma unroll
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     }
 
   // Tiles whose scores need no second look: not the one that the length ends in, none where a column is far.
-  const int plain_tiles = __any_sync(0xffffffffu, far != 0) ? 0 : n / C::TILE;
+  int plain_tiles = __any_sync(0xffffffffu, far != 0) ? 0 : n / C::TILE;
 
   // Outputs, transposed: rows are channels (4-bit: tile 2 g + h holds channels 32 g + 4 r + 2 h and, in rows 8 .. 15, + 1;
   // bf16: 16 c + r and + 8), columns heads.  om: sums of p m.
@@ -595,9 +596,11 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         for (int x = 0; x < NR; ++x)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (far >> (2 * x + (i & 1)) & 1)
 #pragma unroll
-              for (int kt = 0; kt < KT; ++kt) sc[kt][x][i] *= 0x1p126f;
+            for (int kt = 0; kt < KT; ++kt) {
+              if (far >> (2 * x + (i & 1)) & 1) sc[kt][x][i] *= 0x1p126f;
+              if (far >> (4 + 2 * x + (i & 1)) & 1) sc[kt][x][i] *= s_pre[threadIdx.x][2 * x + (i & 1)];
+            }
       }
       const int left = n - tile * C::TILE;  // keys past the length
 #pragma unroll
@@ -656,6 +659,25 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
             o[c][x][2 + y] *= alpha;
           }
         }
+      // sc c2 - m by a fused step would leave the rounding of m: half a unit of it, which beyond 2^20 is no longer small.  There
+      // the products are rounded as m was, from here on.
+      bool big = false;
+#pragma unroll
+      for (int x = 0; x < NR; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          if (fabsf(m_ref[x][y]) > 0x1p20f && m_ref[x][y] != NEG_INF && !(far >> (4 + 2 * x + y) & 1)) {
+            big = true;
+            far |= 16u << (2 * x + y);
+            s_pre[threadIdx.x][2 * x + y] = c2[x][y];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              sc[kt][x][y] *= c2[x][y];
+              sc[kt][x][2 + y] *= c2[x][y];
+            }
+            c2[x][y] = 1.f;
+          }
+      if (__any_sync(0xffffffffu, big)) plain_tiles = 0;
     }
 #pragma unroll
     for (int x = 0; x < NR; ++x)
@@ -780,9 +802,8 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         for (int w = 0; w < C::WARPS; ++w) L = fmaf(sm100::ex2_approx(s_stat[w][row].x - M), s_stat[w][row].y, L);
         const float mul = L == 0.f ? 0.f : sm100::ex2_approx(m_ref[x][y] - M) / L;  // of this warp's sums
         if (warp == 0 && r == 0 && row < heads) {
-          const float l2 = M + log2f(L);
-          p.part_lse[part0 + row] = l2;
-          if (whole && p.LSE) p.LSE[head0 + row] = l2 * 0.69314718055994531f;
+          p.part_stat[part0 + row] = make_float2(L == 0.f ? NEG_INF : M, L);
+          if (whole && p.LSE) p.LSE[head0 + row] = (M + log2f(L)) * 0.69314718055994531f;
         }
         float* to = join + warp * JOIN + row * C::JOIN_ROW;
         if constexpr (KV4) {
@@ -829,7 +850,7 @@ template <int D>
 __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel(const CacheDecodeParams p) {
   constexpr int WARPS = CACHE_FINISH_THREADS / 32;
   __shared__ float s_o[WARPS][D];
-  __shared__ float s_lse[WARPS];
+  __shared__ float2 s_stat[WARPS];  // m, 1 / l
   cudaGridDependencySynchronize();
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int kvh = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -851,19 +872,24 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     const int c0 = line.cta_of(x), c1 = line.cta_of(x + nb - 1);
     return Segments{(size_t)b * p.H_kv * p.head_blocks + unit + c0, c1 - c0 + 1};
   };
-  // Base-2 log-sum-exp of a unit's row, by one warp.
-  auto row_lse = [&](const Segments& g, int row) {
-    const float* lse = p.part_lse + g.first * p.rows + row;
-    if (g.n == 1) return lse[0];
-    float M = NEG_INF, L = 0.f;
-    for (int s = lane; s < g.n; s += 32) M = fmaxf(M, lse[(size_t)s * p.rows]);
+  // A unit's row by one warp: the reference m and the sum l of 2^(score - m) over all segments (0: no key counts).  They stay
+  // apart, as m + log2 l would lose l beside a large m.
+  auto row_stat = [&](const Segments& g, int row) {
+    const float2* stat = p.part_stat + g.first * p.rows + row;
+    const float2 mine = lane < g.n ? stat[(size_t)lane * p.rows] : make_float2(NEG_INF, 0.f);
+    float M = mine.x;
+    for (int s = lane + 32; s < g.n; s += 32) M = fmaxf(M, stat[(size_t)s * p.rows].x);
 #pragma unroll
     for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float m = M == NEG_INF ? 0.f : M;
-    for (int s = lane; s < g.n; s += 32) L += exp2f(lse[(size_t)s * p.rows] - m);
+    if (M == NEG_INF) M = 0.f;
+    float L = exp2f(mine.x - M) * mine.y;
+    for (int s = lane + 32; s < g.n; s += 32) {
+      const float2 x = stat[(size_t)s * p.rows];
+      L = fmaf(exp2f(x.x - M), x.y, L);
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    return m + log2f(L);
+    return make_float2(M, L);
   };
   if (key0 < 0) {
     const int hb = blockIdx.x, heads = min(p.rows, p.group - hb * p.rows);
@@ -880,11 +906,13 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     const int row = warp % p.rows, set = warp / p.rows, sets = WARPS / p.rows;
     float acc[E] = {};
     if (row < heads) {
-      const float l2 = row_lse(g, row), off = l2 == NEG_INF ? 0.f : l2;  // all parts -inf: 2^-inf
+      const float2 stat = row_stat(g, row);
+      const float inv = stat.y == 0.f ? 0.f : 1.f / stat.y;
 #pragma unroll 4
       for (int s = set; s < g.n; s += sets) {
         const size_t part = (g.first + s) * p.rows + row;
-        const float w = exp2f(p.part_lse[part] - off);
+        const float2 x = p.part_stat[part];
+        const float w = exp2f(x.x - stat.x) * x.y * inv;
         const float* v = p.part_o + part * D + lane * E;
         if constexpr (E == 4) {
           const float4 u = *reinterpret_cast<const float4*>(v);
@@ -894,7 +922,7 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
           acc[0] = fmaf(w, u.x, acc[0]), acc[1] = fmaf(w, u.y, acc[1]);
         }
       }
-      if (p.LSE && set == 0 && lane == 0) p.LSE[first_head + row] = l2 * 0.69314718055994531f;
+      if (p.LSE && set == 0 && lane == 0) p.LSE[first_head + row] = (stat.x + log2f(stat.y)) * 0.69314718055994531f;
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) s_o[warp][lane * E + i] = acc[i];
@@ -912,8 +940,8 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
     const int nh = min(WARPS, p.group - h0);
     if (h0) __syncthreads();
     if (warp < nh) {
-      const float x = row_lse(segments((h0 + warp) / p.rows), (h0 + warp) % p.rows);
-      if (lane == 0) s_lse[warp] = x == NEG_INF ? 0.f : x;  // its scores are all -inf: weights of 0
+      const float2 x = row_stat(segments((h0 + warp) / p.rows), (h0 + warp) % p.rows);
+      if (lane == 0) s_stat[warp] = make_float2(x.x, x.y == 0.f ? 0.f : 1.f / x.y);
     }
     __syncthreads();
 #pragma unroll
@@ -924,11 +952,11 @@ __global__ void __launch_bounds__(CACHE_FINISH_THREADS) sdpa_cache_finish_kernel
 #pragma unroll 4
         for (int h = 0; h < nh; ++h) {
           const float4 v = __ldcs(reinterpret_cast<const float4*>(from + (size_t)h * p.score_stride));
-          const float l = s_lse[h];
-          w[y][0] += exp2f(v.x - l);
-          w[y][1] += exp2f(v.y - l);
-          w[y][2] += exp2f(v.z - l);
-          w[y][3] += exp2f(v.w - l);
+          const float2 l = s_stat[h];
+          w[y][0] = fmaf(exp2f(v.x - l.x), l.y, w[y][0]);
+          w[y][1] = fmaf(exp2f(v.y - l.x), l.y, w[y][1]);
+          w[y][2] = fmaf(exp2f(v.z - l.x), l.y, w[y][2]);
+          w[y][3] = fmaf(exp2f(v.w - l.x), l.y, w[y][3]);
         }
       }
     }

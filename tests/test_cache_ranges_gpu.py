@@ -194,3 +194,64 @@ def test_keys_of_minus_infinity(sdpa, d, G, lo, hi):
     for b, h in others:
         at = slice(h * G, h * G + G)
         assert torch.equal(O[b, at], O2[b, at]) and torch.equal(L[b, at], L2[b, at]) and torch.equal(acc[b, h], plain[b, h])
+
+
+# ------------------------------------------------------------------------------------------ scores of any size
+@pytest.mark.parametrize("size", [2, 10, 17, 20, 21, 24, 28, 31, 33, 60, 100, 125])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("G", [1, 12])
+@pytest.mark.parametrize("bits", [4, 16])
+def test_scores_of_any_size(sdpa, bits, G, sign, size):
+    """Scores of up to 2^size, exact in 32 bits: two keys, in two places, share the largest.  Their weights are a half where it is far
+    above the rest, however large it is."""
+    import torch
+    d, n = 64, 300
+    q = torch.full((1, G, d), 2.0 ** (size - 6), device="cuda").to(torch.bfloat16)
+    t = (torch.arange(n) % 13 - 8) / 8.0
+    t[17] = t[200] = 1.0
+    t = t * 2.0 if sign > 0 else (t - 2.0) * 2.0  # the largest: 2, or -2
+    k = t.to("cuda")[:, None].expand(n, d).to(torch.bfloat16).view(1, 1, n, d).contiguous()
+    v = rnd((1, 1, n, d), 3)
+    acc = torch.zeros((1, 1, n), device="cuda")
+    if bits == 4:
+        cache = sdpa.kv4_cache(1, 1, n, d)
+        sdpa.kv4_append(cache, k, v, i32([0]))
+        v64 = values64(cache.v_codes, cache.v_scales)[0, 0]
+        O, L = sdpa.decode_kv4(q, cache, i32([n]), scale=0.5, acc=acc)
+    else:
+        v64 = v[0, 0].double()
+        O, L = sdpa.decode_acc(q, k, v, i32([n]), acc, scale=0.5)
+    s = q[0].double() @ k[0, 0].double().T * 0.5
+    p, lse = torch.softmax(s, -1), torch.logsumexp(s, -1)
+    # a score is exact but for the rounding of scale log2 e; weights that count differ by less than 2^7 in their scores
+    assert ((acc[0, 0].double() - p.sum(0)).abs() <= 2.0 ** -14 * p.sum(0) + G * 2.0 ** -126).all()
+    assert ((L[0].double() - lse).abs() <= 2.0 ** -21 * (1 + lse.abs())).all()
+    want, size_of = p @ v64, p @ v64.abs()
+    # 4 bits: a value is s c + m; its parts are at most 16 times as large
+    assert ((O[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -12 * 16 if bits == 4 else 2.0 ** -12) * size_of).all()
+
+
+@pytest.mark.parametrize("lo,hi", [(0, 128), (128, 384), (0, 511), (0, 512)])
+def test_scores_below_the_range_in_4_bits(sdpa, lo, hi):
+    """Keys whose products are below the least 32-bit number count nothing; without others the outputs are 0 and the LSE -inf."""
+    import torch
+    d, n, G = 128, 512, 4
+    cache = make(sdpa, 4, 1, 1, n, d, [n], 4)
+    q = (rnd((1, G, d), 5).abs().double() * 2.0 ** 60 + 2.0 ** 60).to(torch.bfloat16)
+    scale = 2.0 ** -62
+    cache[1][0, 0, lo:hi, :, 0], cache[1][0, 0, lo:hi, :, 1] = 0.0, -(2.0 ** 120)  # scores of -2^125 or so times 1.44, and of less
+    q[0, 1] = q[0, 1] * 2.0 ** 60
+    acc = torch.zeros((1, 1, n), device="cuda")
+    O, L = sdpa.decode_kv4(q, sdpa.Kv4Cache(*cache), i32([n]), scale=scale, acc=acc)
+    k, v = values64(cache[0], cache[1])[0, 0], values64(cache[2], cache[3])[0, 0]
+    head = 1  # its scores: |q| = 2^120, -2^120 keys: below -2^128 in 32 bits
+    s = q[0].double() @ k.T * scale
+    if hi - lo < n:
+        p = torch.softmax(s, -1)
+        assert torch.isfinite(O).all() and torch.isfinite(L).all() and torch.isfinite(acc).all() and (acc[0, 0, lo:hi] == 0).all()
+        rest = [j for j in range(n) if not lo <= j < hi]
+        big = int(s[head, rest].argmax())
+        assert p[head, rest[big]] > 0.999  # with q this large one key has it all
+        assert torch.allclose(O[0, head].double(), v[rest[big]], rtol=2.0 ** -7, atol=1e-6)
+    else:
+        assert (O[0, head] == 0).all() and L[0, head] == -math.inf
