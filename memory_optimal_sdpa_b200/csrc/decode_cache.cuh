@@ -27,8 +27,10 @@
 // largest and smaller lose bits, far below the rounding of the 32-bit sums).
 //   scores   S[h, j] = sum_g s_jg (sum_{i in g} q_hi c_ji) + m_jg (sum_{i in g} q_hi)
 //   output   O[h, i] = sum_j (p_hj s_jg) c_ji + sum_j p_hj m_jg          (g the group of channel i)
-// p s is rounded to fp16 (half a step: 2^-12 of it, a sixteenth of the rounding of O to bf16), scaled by a power of
-// two that keeps it in range; the sums with m and everything else stay in fp32.
+// p s is rounded to fp16, scaled by a power of two f that the scales of the tile set: 2^-3 <= s f < 2^11, so half a step is 2^-12 of
+// it (a sixteenth of the rounding of O to bf16) for p from 2^-11 on, and below that 2^-22 of s at most.  The sums with m and everything
+// else stay in fp32.  A tile whose scales leave that range moves f; one whose scales are too far apart for any f (an outlier
+// among the rows) is added up in fp32, as the other rows would lose their bits to it.
 // bf16 caches use the same kernel with bf16 products; there p is split in two bf16 parts (its rounding to one
 // would cost as much again as that of O).
 // Both products put the cache on the MMA's side of 16 rows (keys, then channels) and the heads on its side of 8, so
@@ -266,6 +268,8 @@ __device__ __forceinline__ void lds_row(uint32_t addr, float (&x)[N]) {
 // 2^e as a float, e clamped to the normal range.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
 
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
+
 // ------------------------------------------------------------------------------------------ operands
 // Q as the B operand (column: head 8 x + r).  4-bit: per group g and step st (channels i = 2 st, 2 st + 1 of the
 // pieces), the pairs (32 g + 8 t + i, 32 g + 8 t + 4 + i), those of odd i divided by 16; see the file's head.
@@ -348,6 +352,91 @@ __device__ __forceinline__ int cache_granule(int gi) {
   constexpr int GPR = D / 8;
   const int row = gi / GPR;
   return row * (2 * D) + (((gi % GPR) ^ (row & 7)) << 4);
+}
+
+// V's scales of a tile (a lane per key), where some are 0, NaN or outside what p s f may be in fp16: 2^-3 <= s f < 2^11.  Where
+// they lie within 2^10 of each other f moves, and the sums o with it; otherwise (or where o would leave the 32-bit range)
+// the result is true and the tile is added up in fp32.
+template <int D, int NR>
+__device__ __forceinline__ bool cache_move_scale(const float (&sv)[D / 32], float& f, float (&o)[D / 16][NR][4]) {
+  uint32_t top = 0, least = 0x7F800000u;
+#pragma unroll
+  for (int g = 0; g < D / 32; ++g) {
+    const uint32_t bits = __float_as_uint(fabsf(sv[g]));
+    if (bits <= 0x7F800000u) top = max(top, bits);  // a NaN stays one in every product
+    if (bits) least = min(least, bits);
+  }
+  const float hi = __uint_as_float(__reduce_max_sync(0xffffffffu, top)), lo = __uint_as_float(__reduce_min_sync(0xffffffffu, least));
+  const bool near = lo * 0x1p10f > hi, none = f != f;
+  const int want = min(7 - exponent_of(near ? hi : lo), 126), room = 100 - exponent_of(hi);  // room: p s f c in 32 bits
+  auto fits = [&] { return hi * f < 0x1p11f && lo * f >= 0x1p-3f; };
+  if (none) {  // no sums yet
+    f = hi > 0.f ? exp2_int(min(want, room)) : 1.f;
+    return hi > 0.f && !fits();
+  }
+  if (hi == 0.f || fits()) return false;
+  const int old = exponent_of(f);
+  float most = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(o[c][x][i]));
+  const int e = min(__all_sync(0xffffffffu, near && exponent_of(most) + want - old < 100) ? want : old, room);
+  const float m0 = exp2_int((e - old) / 2), m1 = exp2_int(e - old - (e - old) / 2);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+    for (int x = 0; x < NR; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[c][x][i] = o[c][x][i] * m0 * m1;
+  f = exp2_int(e);
+  return !fits();
+}
+
+// Adds a tile's p s c, p = 2^(sc c2 - m), to o in fp32, in the units of the products that it stands in for; about five times as
+// slow as they.
+template <int D, int NR>
+__device__ __forceinline__ void cache_add_values(const float (&sc)[2][NR][4], const float (&c2)[NR][2], const float (&m)[NR][2],
+                                                 float (&o)[D / 16][NR][4], uint32_t sV, uint32_t scales, int lane) {
+  constexpr int NG = D / 32;
+  const int r = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (int row = 0; row < 32; ++row) {
+    uint32_t w[NG / 2];
+    if constexpr (D == 128) {
+      const uint2 v = lds<uint2>(sV + cache_granule<D, true>(row * 4 + (r >> 1)) + (r & 1) * 8);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = lds<uint32_t>(sV + cache_granule<D, true>(row * 2 + (r >> 2)) + (r & 3) * 4);
+    }
+    float s[NG];
+    lds_row<NG>(scales + (uint32_t)(row * NG * 4), s);
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      float a[2];  // this key's p; its score is in the lane that has row's place in eight
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float lower = row & 8 ? sc[0][x][2 + y] : sc[0][x][y], upper = row & 8 ? sc[1][x][2 + y] : sc[1][x][y];
+        const float s = __shfl_sync(0xffffffffu, row & 16 ? upper : lower, 4 * (row & 7) + t);
+        a[y] = sm100::ex2_approx(fmaf(s, c2[x][y], m[x][y] == -__int_as_float(0x7f800000) ? 0.f : -m[x][y]));
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t c = w[g >> 1] >> (16 * (g & 1));  // four channels
+        const float a0 = a[0] * s[g] * 0x1p-24f, a1 = a[1] * s[g] * 0x1p-24f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float c0 = (float)(c >> (8 * h) & 0x0Fu), c1 = (float)(c >> (8 * h) & 0xF0u);
+          o[2 * g + h][x][0] = fmaf(a0, c0, o[2 * g + h][x][0]);
+          o[2 * g + h][x][1] = fmaf(a1, c0, o[2 * g + h][x][1]);
+          o[2 * g + h][x][2] = fmaf(a0, c1, o[2 * g + h][x][2]);
+          o[2 * g + h][x][3] = fmaf(a1, c1, o[2 * g + h][x][3]);
+        }
+      }
+    }
+  }
 }
 
 template <int D, bool KV4, bool WIDE>
@@ -483,12 +572,12 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
     for (int x = 0; x < NR; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][x][i] = 0.f;
-  int f_exp = 1000;  // 4-bit: p s is multiplied by 2^f_exp (1000: not chosen yet)
-  float f = 0.f;
+  float f = __int_as_float(0x7FC00000);  // 4-bit: p s is multiplied by this power of two (NaN: not chosen yet)
 
   uint32_t get = 0;  // this tile's stage, in bytes
   for (int tile = warp; tile < n_tiles; tile += C::WARPS) {
     cp_async_wait<C::STAGES - 2>();
+    bool uneven = false;  // 4-bit: V's scales of this tile are too far apart for fp16
     if constexpr (KV4) {
       __syncwarp();  // the last tile's scales have been read
       // The scales for the whole warp, [key][group] of K's s, V's s, V's m; K's m are taken from where they are.
@@ -498,27 +587,15 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
       uint32_t w0[NG], w1[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) w0[g] = __float_as_uint(w0f[g]), w1[g] = __float_as_uint(w1f[g]);
-      float sv[NG], top = 0.f;
+      float sv[NG];
+      const uint32_t least = 0x3E000000u + 0x3F800000u - __float_as_uint(f);  // 2^-3 / f
+      uint32_t beside = 0;  // how far up from there s is, in bits
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         sv[g] = __uint_as_float(w1[g] << 16);
-        top = fmaxf(top, fabsf(sv[g]));  // NaN scales do not count
+        beside = max(beside, (w1[g] << 16) - least);
       }
-      if (__any_sync(0xffffffffu, top * f >= 0x1p11f || f_exp == 1000)) {
-        const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23) - 127;
-        const int f_new = min(9 - e, 126);
-        if (f_exp != 1000) {
-          const float down = f_new - f_exp < -126 ? 0.f : exp2_int(f_new - f_exp);
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int x = 0; x < NR; ++x)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[c][x][i] *= down;
-        }
-        f_exp = f_new;
-        f = exp2_int(f_exp);
-      }
+      if (__any_sync(0xffffffffu, beside >= 0x07000000u || f != f)) uneven = cache_move_scale<D, NR>(sv, f, o);
       const uint32_t to = scales0 + (uint32_t)(lane * NG * 4);
       float k[NG], mv[NG];
 #pragma unroll
@@ -640,6 +717,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
         mt[x][y] = m * c2[x][y];
         move |= mt[x][y] > m_ref[x][y] + 4.f;
       }
+    if (KV4) move |= uneven;
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int x = 0; x < NR; ++x)
@@ -678,6 +756,15 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
             c2[x][y] = 1.f;
           }
       if (__any_sync(0xffffffffu, big)) plain_tiles = 0;
+      if constexpr (KV4)
+        if (uneven) {  // the tile's values now, and nothing of them below
+          const uint32_t at = scales0 + C::TILE * NG * 4;
+          cache_add_values<D, NR>(sc, c2, m_ref, o, sV, at, lane);
+          __syncwarp();
+          const float none[NG] = {};
+          sts_row<NG>(at + (uint32_t)(lane * NG * 4), none);
+          __syncwarp();
+        }
     }
 #pragma unroll
     for (int x = 0; x < NR; ++x)
@@ -785,8 +872,7 @@ __global__ void __launch_bounds__(CacheCfg<D, KV4, WIDE>::THREADS, CacheCfg<D, K
   constexpr int JOIN = C::JOIN_BYTES / 4;
   const bool whole = n_blocks == seq_blocks;  // the unit has no other segment
   {
-    // 4-bit: back from 2^f_exp and 2^-24, in two exact steps
-    const int back = f_exp == 1000 ? 0 : 24 - f_exp;
+    const int back = 24 - exponent_of(f);  // 4-bit: from f and 2^-24, in two exact steps
     const float b0 = exp2_int(back / 2), b1 = exp2_int(back - back / 2);
 #pragma unroll
     for (int x = 0; x < NR; ++x)

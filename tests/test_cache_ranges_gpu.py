@@ -255,3 +255,79 @@ def test_scores_below_the_range_in_4_bits(sdpa, lo, hi):
         assert torch.allclose(O[0, head].double(), v[rest[big]], rtol=2.0 ** -7, atol=1e-6)
     else:
         assert (O[0, head] == 0).all() and L[0, head] == -math.inf
+
+
+# ------------------------------------------------------------------------------------------ values of unlike size
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 20, 2.0 ** 24, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("at", [(0,), (3,), (40,), (149,), (0, 33, 64, 96), (5, 6, 7, 8, 9, 10, 149)])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (64, 12)])
+def test_values_of_a_key_that_counts_nothing(sdpa, d, G, ratio, at):
+    """Values `ratio` times as large as the others', with a weight of (nearly) 0, leave the other keys' as exact as they were."""
+    import torch
+    cache = make(sdpa, 4, 1, 1, 150, d, [150], 7)
+    q = rnd((1, G, d), 8)
+    q[..., 0] = q[..., 0].abs() + 2
+    for j in at:  # -960 in channel 0, else 0: far below every other score
+        cache[0][0, 0, j] = 255
+        cache[0][0, 0, j, 0] = 240
+        cache[1][0, 0, j] = 0
+        cache[1][0, 0, j, 0, 0], cache[1][0, 0, j, 0, 1] = 64.0, -960.0
+        cache[3][0, 0, j] *= ratio
+    check(sdpa, q, cache, [150], 0.25)
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 25, 2.0 ** -25, 2.0 ** 40])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 16)])
+def test_groups_of_channels_of_unlike_size(sdpa, d, G, ratio):
+    import torch
+    cache = make(sdpa, 4, 1, 1, 300, d, [300], 9)
+    cache[3][..., 1, :] *= ratio
+    check(sdpa, rnd((1, G, d), 10), cache, [300], d ** -0.5)
+    assert torch.isfinite(cache[3]).all()
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 12, 2.0 ** 25, 2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("every", [1, 2, 7, 32, 64])
+@pytest.mark.parametrize("d,G", [(64, 2), (128, 8)])
+def test_values_of_unlike_size_that_count(sdpa, d, G, ratio, every):
+    """Large and small rows in turn, by rows and by stretches of rows, all with weight: the large ones set what is exact."""
+    cache = make(sdpa, 4, 1, 1, 520, d, [520], 11)
+    for j in range(520):
+        if (j // every) % 2:
+            cache[3][0, 0, j] *= ratio
+    check(sdpa, rnd((1, G, d), 12), cache, [520], d ** -0.5)
+    flipped = list(cache)
+    flipped[3] = cache[3].clone()
+    flipped[3][0, 0] = cache[3][0, 0].flip(0)
+    check(sdpa, rnd((1, G, d), 12), flipped, [520], d ** -0.5)
+
+
+def test_rows_of_one_value(sdpa):
+    """Groups whose channels are all equal have a scale of 0, some rows, whole stretches or the whole cache."""
+    import torch
+    d, n = 128, 400
+    q = rnd((1, 4, d), 13)
+    for rows in (slice(0, 1), slice(3, 200), slice(0, n), slice(390, n)):
+        cache = make(sdpa, 4, 1, 1, n, d, [n], 14)
+        cache[3][0, 0, rows, :, 0] = 0.0
+        check(sdpa, q, cache, [n], d ** -0.5)
+        cache[3][0, 0, rows, 1, 0] = 3.0
+        check(sdpa, q, cache, [n], d ** -0.5)
+    cache = make(sdpa, 4, 1, 1, n, d, [n], 15)
+    cache[3][..., 0] = torch.where(rnd((1, 1, n, d // 32), 16).float() > 0, 0.0, 2.0 ** -100)  # and the smallest scales
+    cache[3][..., 1] = 0.0
+    check(sdpa, q, cache, [n], d ** -0.5)
+
+
+def test_an_undefined_row_of_values(sdpa):
+    """A row whose values are NaN reaches the channels of its groups in the heads that see it, and nothing else."""
+    import torch
+    d, n = 128, 200
+    q, cache = rnd((1, 8, d), 17), make(sdpa, 4, 1, 2, n, d, [n], 18)
+    acc, acc2 = (torch.zeros((1, 2, n), device="cuda") for _ in range(2))
+    O, L = sdpa.decode_kv4(q, sdpa.Kv4Cache(*cache), i32([n]), acc=acc)
+    cache[3][0, 1, 77, 2] = float("nan")
+    O2, L2 = sdpa.decode_kv4(q, sdpa.Kv4Cache(*cache), i32([n]), acc=acc2)
+    assert torch.isnan(O2[0, 4:, 64:96]).all() and torch.equal(L, L2) and torch.equal(acc, acc2)
+    O2[0, 4:, 64:96] = O[0, 4:, 64:96]
+    assert torch.equal(O, O2)
