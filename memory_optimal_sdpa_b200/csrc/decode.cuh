@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(DECODE_THREADS) sdpa_decode_split_kernel(const
     float a = 0.f;
     for (int i = 0; i < G; ++i)
       if (s_m[i] != NEG_INF) a += s_acc[i][e] * exp2f(s_m[i] - M);
-    p.part_o[part * D + e] = a / L;
+    p.part_o[part * D + e] = L == 0.f ? 0.f : a / L;  // 0: every key of the split scores -inf
   }
   if (threadIdx.x == 0) p.part_lse[part] = M * 0.69314718055994531f + logf(L);
 }
@@ -186,15 +186,16 @@ __global__ void __launch_bounds__(D) sdpa_decode_combine_kernel(const DecodePara
   const float* lse = p.part_lse + (size_t)bh * p.n_split;
   float M = -__int_as_float(0x7f800000);
   for (int s = 0; s < ns; ++s) M = fmaxf(M, lse[s]);
+  const float m = M == -__int_as_float(0x7f800000) ? 0.f : M;  // every key scores -inf: O = 0, LSE = -inf
   float L = 0.f, a = 0.f;
   const int e = threadIdx.x;
   const float* po = p.part_o + (size_t)bh * p.n_split * D + e;
   for (int s = 0; s < ns; ++s) {
-    const float w = __expf(lse[s] - M);
+    const float w = __expf(lse[s] - m);
     L += w;
     a = fmaf(w, po[(size_t)s * D], a);
   }
-  p.O[(size_t)bh * D + e] = __float2bfloat16_rn(a / L);
+  p.O[(size_t)bh * D + e] = __float2bfloat16_rn(L == 0.f ? 0.f : a / L);
   if (p.LSE && e == 0) p.LSE[bh] = M + logf(L);
 }
 

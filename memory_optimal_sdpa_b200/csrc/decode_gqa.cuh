@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(192, GqaCfg<NQ>::MIN_BLOCKS)
         if (g < G) {
           const float l = red[g] + red[NQ + g] + red[2 * NQ + g] + red[3 * NQ + g];
           const size_t part = ((size_t)(b * p.H_q + kvh * G + g)) * p.n_split + s;
-          p.part_o[part * 128 + row] = __uint_as_float(o[g]) / l;  // row = output dimension here
+          p.part_o[part * 128 + row] = l == 0.f ? 0.f : __uint_as_float(o[g]) / l;  // row = output dimension here; 0: all keys score -inf
           if (row == g) p.part_lse[part] = (m_ref[g] + log2f(l)) * 0.69314718055994531f;
         }
       }
