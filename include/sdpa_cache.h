@@ -12,8 +12,8 @@
  * Conventions of sdpa.h hold: contiguous row-major caller-owned device memory, 16-byte aligned where
  * not said otherwise, asynchronous on `stream`, nothing allocated, argument checks before any launch,
  * device-side problems in the device error word (a length outside its range is clamped and recorded
- * as SDPA_ERR_DEVICE_BAD_LENGTH), batch == 0 or heads == 0 -> SDPA_OK.  d is 64 or 128, else
- * SDPA_ERR_UNSUPPORTED.  Unlike sdpa_decode, lengths may be 0 here (an empty slot of a padded batch).
+ * as SDPA_ERR_DEVICE_BAD_LENGTH), batch == 0 or heads == 0 -> SDPA_OK and nothing is written.  d is 64 or 128,
+ * else SDPA_ERR_UNSUPPORTED.  Unlike sdpa_decode, lengths may be 0 here (an empty slot of a padded batch).
  * int32 and float arrays (lengths, LSE, weights, kept rows) need 4-byte alignment only.
  * batch * heads * rows of every array is at most 2^31 - 8192, batch and heads are at most 65535.
  *

@@ -391,6 +391,12 @@ def _both(name, a, b):
         raise ValueError("give both of %s or neither" % name)
 
 
+def _some_heads(name, heads):
+    """Refuse calls without a head that would have to fill an output: the library writes nothing then."""
+    if heads == 0:
+        raise ValueError("%s must have at least one head" % name)
+
+
 def _made(stream, make):
     """make() with its tensors made (and filled) on `stream` (None: the current one)."""
     import torch
@@ -501,6 +507,8 @@ def _decode_run(where, size, q, keys, names, kv_lens, B, H_kv, n_cap, d, scale, 
     import torch
     H_q = _free(q, "q", torch.bfloat16, 3)[1]
     _fit(q, "q", torch.bfloat16, (B, H_q, d))
+    if acc_out is not None:
+        _some_heads("q", H_q)
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
     if o is not None:
         _fit(o, "o", torch.bfloat16, q.shape)
@@ -568,6 +576,7 @@ def fwd_acc(q, k, lse, acc=None, causal=False, scale=None, acc_out=None, stream=
     Returns acc_out."""
     import torch
     B, H_q, n_q, d = _free(q, "q", torch.bfloat16, 4)
+    _some_heads("q", H_q)
     _, H_kv, n_kv, _ = _free(k, "k", torch.bfloat16, 4)
     _fit(k, "k", torch.bfloat16, (B, H_kv, n_kv, d))
     _fit(lse, "lse", torch.float32, (B, H_q, n_q))
@@ -585,6 +594,7 @@ def _evict_run(where, arrays, outs, names, out_names, acc, kv_lens, budget, rece
     """The part that evict and kv4_evict share; outs None: in place."""
     import torch
     budget, recent = int(budget), int(recent)
+    _some_heads(names[0], H)
     _fit(acc, "acc", torch.float32, (B, H, n_cap))
     _fit(kv_lens, "kv_lens", torch.int32, (B,))
     if (outs is None) != (acc_out is None):
