@@ -47,7 +47,7 @@ extern "C" {
  * s = m = NaN and reads back as NaN.
  * k_read, v_read [batch, heads, n_rows, d] bf16, or both NULL: the values the cache now stands for,
  * s c + m rounded to bf16, for the attention of the rows' own step (rows t >= n_new[b] are left as
- * they were).  They may not overlap K or V (SDPA_ERR_INVALID_ARG).
+ * they were).  They may not overlap K, V or each other (SDPA_ERR_INVALID_ARG).
  */
 SDPA_API int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens, const int* n_new, void* k_codes,
                              void* k_scales, void* v_codes, void* v_scales, void* k_read, void* v_read, int batch,
@@ -72,7 +72,7 @@ SDPA_API int sdpa_kv4_load(const void* k_codes, const void* k_scales, const void
  * acc_out [batch, heads_kv, n_kv_cap] float or NULL:
  *     acc_out[b, g, j] = acc[b, g, j] + sum over the query heads h of group g of exp(scale q_h . k_j - LSE_h)
  * for j < kv_lens[b]; entries at or past kv_lens[b] are left as they were.  acc may be acc_out (the usual
- * running sum) or NULL (zeros); acc without acc_out is SDPA_ERR_INVALID_ARG.
+ * running sum) or NULL (zeros); acc without acc_out, or overlapping it in part, is SDPA_ERR_INVALID_ARG.
  * workspace: sdpa_decode_kv4_workspace_size bytes (with_acc: whether acc_out is given), scratch.  Calls that may run at
  * the same time (other streams, graphs replayed side by side) need one each.
  */
@@ -99,7 +99,7 @@ SDPA_API int sdpa_decode_acc(const void* Q, const void* K, const void* V, const 
  * sdpa_fwd wrote it for the same scale and mask (a query with LSE = -inf or +inf adds nothing).  causal is
  * bottom-right aligned, so the last n_q queries of a longer prompt may be given alone.  acc, acc_out
  * [batch, heads_kv, n_acc], n_acc >= n_kv (the decode cache's capacity); entries at or past n_kv are left
- * as they were; acc may be acc_out or NULL (zeros).  n_q == 0 copies acc.
+ * as they were; acc may be acc_out (not overlap it in part) or NULL (zeros).  n_q == 0 copies acc.
  */
 SDPA_API int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, const float* acc, float* acc_out, int batch,
                           int heads_q, int heads_kv, int n_q, int n_kv, int n_acc, int d, float scale, int causal,
@@ -117,7 +117,7 @@ SDPA_API int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, const 
  * new_lens[b] (rows appended later start at 0).
  * Every output array (acc_out included) is either its input (in place; then n_out_cap == n_kv_cap) or does
  * not overlap any input.  1 <= budget <= n_out_cap, 0 <= recent <= budget, 0 <= kv_lens[b] <= n_kv_cap;
- * new_lens may not be kv_lens.
+ * keep and new_lens overlap no other array.
  */
 SDPA_API int sdpa_evict(const void* K, const void* V, const float* acc, const int* kv_lens, void* K_out, void* V_out,
                         float* acc_out, int* keep, int* new_lens, int batch, int heads, int n_kv_cap, int n_out_cap,

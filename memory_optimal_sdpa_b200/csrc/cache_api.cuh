@@ -73,6 +73,11 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
 }
 
+// A running sum goes into its own place or elsewhere: an array that overlaps it partly would be read after it was written.
+bool sums_fit(const float* acc, const float* acc_out, size_t n) {
+  return !acc || acc == acc_out || !overlap(acc, n * sizeof(float), acc_out, n * sizeof(float));
+}
+
 bool cache_arrays_aligned(const void* kc, const void* ks, const void* vc, const void* vs) {
   return aligned16(kc) && aligned16(ks) && aligned16(vc) && aligned16(vs);
 }
@@ -94,6 +99,7 @@ extern "C" int sdpa_kv4_append(const void* K, const void* V, const int* kv_lens,
   const size_t bytes = (size_t)batch * heads * n_rows * d * 2;
   for (const void* read : {k_read, v_read})  // the inputs are read through the non-coherent path
     if (read && (overlap(read, bytes, K, bytes) || overlap(read, bytes, V, bytes))) return SDPA_ERR_INVALID_ARG;
+  if (k_read && overlap(k_read, bytes, v_read, bytes)) return SDPA_ERR_INVALID_ARG;
   if (int e = check_device()) return e;
   sdpa::Kv4RowsParams p = {};
   p.cache[0] = {(uint8_t*)k_codes, (uint32_t*)k_scales};
@@ -213,6 +219,7 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   if (!aligned16(Q) || !aligned16(O) || !aligned4(kv_lens) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out))
     return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads_q, 1) || !cache_sizes_fit(batch, heads_kv, n_cap)) return SDPA_ERR_UNSUPPORTED;
+  if (!sums_fit(acc, acc_out, (size_t)batch * heads_kv * n_cap)) return SDPA_ERR_INVALID_ARG;
   const size_t need = cache_ws_size(batch, heads_q, heads_kv, n_cap, d, kv4, acc_out != nullptr);
   if (!workspace || workspace_bytes < need) return SDPA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return SDPA_ERR_MISALIGNED;
@@ -327,6 +334,7 @@ extern "C" int sdpa_fwd_acc(const void* Q, const void* K, const float* LSE, cons
   if (!K || !acc_out || (n_q > 0 && (!Q || !LSE))) return SDPA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(K) || !aligned4(LSE) || !aligned4(acc) || !aligned4(acc_out)) return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads_q, n_q) || !cache_sizes_fit(batch, heads_kv, n_acc)) return SDPA_ERR_UNSUPPORTED;
+  if (!sums_fit(acc, acc_out, (size_t)batch * heads_kv * n_acc)) return SDPA_ERR_INVALID_ARG;
   if (int e = check_device()) return e;
   sdpa::PromptWeightsParams p = {};
   p.LSE = LSE;
@@ -372,7 +380,18 @@ int evict(const EvictArray* arrays, int n, const float* acc, const int* kv_lens,
   if (!kv_lens || !keep || !new_lens) return SDPA_ERR_INVALID_ARG;
   if (!aligned4(kv_lens) || !aligned4(keep) || !aligned4(new_lens)) return SDPA_ERR_MISALIGNED;
   if (!cache_sizes_fit(batch, heads, n_cap) || !cache_sizes_fit(batch, heads, n_out)) return SDPA_ERR_UNSUPPORTED;
-  if (overlap(kv_lens, (size_t)batch * 4, new_lens, (size_t)batch * 4)) return SDPA_ERR_INVALID_ARG;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } results[2] = {{keep, bh * budget * 4}, {new_lens, (size_t)batch * 4}};
+  for (const auto& r : results) {  // they overlap nothing
+    if (overlap(r.at, r.bytes, kv_lens, (size_t)batch * 4)) return SDPA_ERR_INVALID_ARG;
+    for (int i = 0; i <= n; ++i)
+      if (overlap(r.at, r.bytes, all[i].in, bh * n_cap * all[i].row_bytes) ||
+          overlap(r.at, r.bytes, all[i].out, bh * n_out * all[i].row_bytes))
+        return SDPA_ERR_INVALID_ARG;
+  }
+  if (overlap(keep, results[0].bytes, new_lens, results[1].bytes)) return SDPA_ERR_INVALID_ARG;
   for (int i = 0; i <= n; ++i)  // an output is its own input or apart from every input and output
     for (int j = 0; j <= n; ++j) {
       const bool in_place = i == j && all[i].in == all[i].out && n_out == n_cap;

@@ -28,3 +28,24 @@ def test_no_heads_to_fill_an_output_from():
                  lambda: sdpa.kv4_evict(cache(H=0), t(2, 0, 8, dtype=f32), LENS, 4)):
         with pytest.raises(ValueError, match="at least one head"):
             call()
+
+
+def test_sums_that_overlap_in_part():
+    """acc and acc_out are one array or apart; so are the rows read back, and what an eviction returns."""
+    P, FAR, inv = 0x10000, 1 << 40, sdpa.SDPA_ERR_INVALID_ARG
+    lib, size = sdpa.lib, 2 * 8 * 4  # two heads, eight rows
+    for out in (P + 4, P + size - 4, P - 4):
+        assert lib.sdpa_decode_acc(FAR, FAR, FAR, FAR, FAR, None, P, out, 1, 2, 2, 8, 64, 0.1, FAR, 1 << 30, None) == inv
+        assert lib.sdpa_decode_kv4(FAR, FAR, FAR, FAR, FAR, FAR, FAR, None, P, out, 1, 2, 2, 8, 64, 0.1, FAR, 1 << 30, None) == inv
+        assert lib.sdpa_fwd_acc(FAR, FAR, FAR, P, out, 1, 2, 2, 4, 8, 8, 64, 0.1, 0, None) == inv
+    # apart, or one: the arguments are right (what is refused next is the missing workspace, or the device here)
+    for out in (P, P + size, P - size):
+        assert lib.sdpa_decode_acc(FAR, FAR, FAR, FAR, FAR, None, P, out, 1, 2, 2, 8, 64, 0.1, None, 0, None) == sdpa.SDPA_ERR_WORKSPACE
+    rows = 2 * 3 * 64 * 2
+    for read in (P + 16, P + rows - 16):
+        assert lib.sdpa_kv4_append(FAR, 2 * FAR, FAR, None, FAR, FAR, FAR, FAR, P, read, 1, 2, 3, 8, 64, None) == inv
+
+    def evict(keep, new, lens=3 * FAR):
+        return lib.sdpa_evict(FAR, 2 * FAR, 4 * FAR, lens, FAR, 2 * FAR, 4 * FAR, keep, new, 1, 2, 8, 8, 64, 4, 1, None)
+    assert evict(FAR + 64, 5 * FAR) == inv and evict(4 * FAR, 5 * FAR) == inv and evict(3 * FAR, 5 * FAR) == inv
+    assert evict(5 * FAR, 5 * FAR + 4) == inv and evict(5 * FAR, 2 * FAR) == inv
