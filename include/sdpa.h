@@ -74,7 +74,8 @@ typedef enum {
  * negate-A bit), so the online softmax always works with |scale|; scale == 0 gives every
  * visible key weight 1 / (number of visible keys) and LSE = ln(number of visible keys)
  * (computed with the factor 2^-126 in place of 0, which leaves every weight exactly 1 in
- * fp32 for scores below 2^100 in magnitude and keeps masked entries at weight 0).
+ * fp32 for scores below 2^100 in magnitude and keeps masked entries at weight 0).  Magnitudes
+ * above 2.35e38 (the largest float over log2 e) count as that, in the decodes too.
  * Every pointer 16-byte aligned (TMA), else SDPA_ERR_MISALIGNED.
  * Arithmetic: S = Q K^T and O += P V on the tensor cores with fp32
  * accumulation; softmax in fp32 with P rounded to bf16; O rounded to bf16

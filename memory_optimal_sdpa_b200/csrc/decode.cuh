@@ -72,7 +72,8 @@ struct DecodeParams {
   float* LSE;              // [B, H] or null
   int H, n_cap, chunk, n_split;
   int H_kv, group;         // H = H_kv * group; group 1 is plain multi-head decode
-  float scale_log2;        // scale * log2(e)
+  float scale_log2;        // scale * log2(e): what q is multiplied by ...
+  float scale_after;       // ... and q . k (1, unless the scale is so large that q would overflow)
 };
 
 template <int D>
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(DECODE_THREADS) sdpa_decode_split_kernel(const
       for (int i = 0; i < 8; ++i) d = fmaf(q[i], kf[i], d);
 #pragma unroll
       for (int off = LPK / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      sc[u] = (base + u * G + g < k_end) ? d : NEG_INF;
+      sc[u] = (base + u * G + g < k_end) ? d * p.scale_after : NEG_INF;
     }
     float mx = sc[0];
 #pragma unroll

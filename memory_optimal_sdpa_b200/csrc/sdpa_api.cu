@@ -98,6 +98,19 @@ int sm_count() {
     return 148;
   return n;
 }
+// scale log2 e, which the largest scales (above 2.36e38) would take out of range: a score of 0 would become NaN.
+float times_log2e(float scale) {
+  const float x = scale * 1.4426950408889634f;
+  return std::isfinite(x) ? x : std::copysign(FLT_MAX, scale);
+}
+
+// The factors of q and of q . k, one of them 1: q takes the whole where that cannot overflow.
+void decode_scale(sdpa::DecodeParams& p, float scale) {
+  const float x = times_log2e(scale);
+  p.scale_log2 = std::fabs(x) < 0x1p64f ? x : 1.f;
+  p.scale_after = std::fabs(x) < 0x1p64f ? 1.f : x;
+}
+
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 // The current device must be an sm_100 part (B200 class).
@@ -136,7 +149,7 @@ int launch_prefill(const void* Q, const void* K, const void* V, void* O, float* 
   // scale = 0 runs with the smallest normal float as the factor: every finite score s then gets
   // 2^(s * 2^-126 - m) = 1 exactly in fp32 (|s| < 2^100), the weights are uniform as the definition
   // says, and masked entries (-inf) still give 0, where a factor of exactly 0 would give -inf * 0 = NaN.
-  p.scale_log2 = scale == 0.f ? FLT_MIN : std::fabs(scale) * 1.4426950408889634f;
+  p.scale_log2 = scale == 0.f ? FLT_MIN : std::fabs(times_log2e(scale));
   p.negate_s = scale < 0.f ? 1 : 0;
   p.win_left = win_left;
   p.win_right = win_right;
@@ -270,7 +283,7 @@ extern "C" int sdpa_decode(const void* Q, const void* K, const void* V, const in
   p.part_lse = p.part_o + (size_t)batch * heads * p.n_split * d_v;
   p.O = (__nv_bfloat16*)O;
   p.LSE = LSE;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  decode_scale(p, scale);
   cudaStream_t s = (cudaStream_t)stream;
   dim3 grid((unsigned)p.n_split, (unsigned)heads, (unsigned)batch);
   if (d_k == 64) {
@@ -367,7 +380,7 @@ extern "C" int sdpa_decode_noalloc(const void* Q, const void* K, const void* V, 
   p.part_lse = scratch + (size_t)bh * p.n_split * d_v;
   p.O = (__nv_bfloat16*)O;
   p.LSE = LSE;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  decode_scale(p, scale);
   cudaStream_t s = (cudaStream_t)stream;
   dim3 grid((unsigned)p.n_split, (unsigned)heads, (unsigned)batch);
   if (d_k == 64) {
@@ -424,7 +437,7 @@ int launch_decode_gqa(const void* Q, const void* K, const void* V, const int* kv
   p.n_cap = n_cap;
   p.chunk = chunk;
   p.n_split = n_split;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = times_log2e(scale);
   dim3 grid((unsigned)n_split, (unsigned)heads_kv, (unsigned)batch);
   kern<<<grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(mq, mk, mv, p);
   const cudaError_t e = cudaGetLastError();
@@ -474,7 +487,7 @@ extern "C" int sdpa_decode_gqa(const void* Q, const void* K, const void* V, cons
   p.part_lse = p.part_o + (size_t)batch * heads_q * p.n_split * d_v;
   p.O = (__nv_bfloat16*)O;
   p.LSE = LSE;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  decode_scale(p, scale);
   cudaStream_t s = (cudaStream_t)stream;
   if (gqa_tensor_path(group, d_k)) {
     const int rc = group <= 16
