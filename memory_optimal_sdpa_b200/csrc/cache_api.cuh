@@ -297,9 +297,17 @@ extern "C" int sdpa_decode_acc(const void* Q, const void* K, const void* V, cons
 // ------------------------------------------------------------------ weights of a prompt
 namespace {
 
-// Units of 256 keys where there is one for every SM, else of 128 (both measured at the head of prompt_weights.cuh).
+// Units of 256 keys unless the heaviest one, which sees all queries, is more than 15 % above an SM's share of the 128 x 128
+// tiles: then of 128 (both measured at the head of prompt_weights.cuh).
 bool prompt_wide(const sdpa::PromptWeightsParams& p) {
-  return (long long)p.bkv * ((p.n_kv + 255) / 256) >= 148;
+  const long long n_kt = (p.n_kv + 127) / 128, n_qt = (p.n_q + 127) / 128;
+  long long tiles = n_kt * n_qt;  // of a head
+  if (p.causal) {                 // key tile k loses max(0, k - k0) query tiles
+    const long long off = (long long)p.n_kv - p.n_q, k0 = off >= 0 ? (off + 127) / 128 : -(-off / 128);
+    const long long most = n_kt - 1 - k0, least = k0 < 0 ? -k0 : 0;
+    if (most > 0) tiles -= (most * (most + 1) - least * (least - 1)) / 2;
+  }
+  return 2.0 * (double)n_qt * sm_count() <= 1.15 * (double)tiles * p.bkv;
 }
 
 template <int D, int MT>

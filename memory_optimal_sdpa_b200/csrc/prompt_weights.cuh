@@ -8,9 +8,12 @@
 // running maximum, no exchange between threads, no atomics; the order of the sums is fixed.
 //
 // A unit of work is 128 MT keys of one (sequence, key/value head); its queries stream past in tiles of 128, head
-// after head.  MT = 2 halves the waits of the producer and the MMA issuer and the L2 traffic of the queries; MT = 1 is
-// for fewer than 148 units of 256 keys.  Measured, MT = 2 against 1: 32 heads over 8, n = 8192, causal 352 and 369 us; the last 64
-// queries of 4 x 16 heads, 16001 keys, d = 64 45 and 57 us when this was chosen (44 us now).  What bounds it: for many queries the exponentials (16
+// after head.  MT = 2 halves the waits of the producer and the MMA issuer and the L2 traffic of the queries, but a unit is
+// the least that an SM can be given: MT = 1 where the heaviest unit of 256 keys, which sees all queries, is more than 15 % above an
+// SM's share.  Measured, MT = 2 against 1, us (causal, calls back to back): 32 heads over 8, d = 128, n = 4096 175 and 94, 6000 256
+// and 198, 7000 296 and 260, 8192 (14 % above) 340 and 344, 9472 423 and 442, 32768 5111 and 5388; the last 64 queries of
+// 2 x 32 heads over 8, 16001 keys 39 and 47, the last 512 162 and 166; of 4 x 16 heads, d = 64, 16001 keys 45 and 55, of 1 x 32 heads over 8,
+// 2000 keys 14.3 and 12.3.  What bounds it: for many queries the exponentials (16
 // per clock and SM on the MUFU unit, so 1024 clocks for 128 x 128 scores, against 512 for the MMA at d = 128; 239 us for the
 // former case, whose heaviest unit is also 12 % above an SM's share).  For few queries the hand-offs of a
 // unit and its exponentials in a chain (about 3000 clocks for 256 keys and 64 queries), not HBM (21 us for the latter case).

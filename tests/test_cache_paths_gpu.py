@@ -198,3 +198,27 @@ def test_calls_beside_a_replayed_graph(sdpa):
     assert torch.equal(state[1], alone[1]) and all(torch.equal(x, y) for x, y in zip(state[0], alone[0]))
     for r in beside:
         assert all(torch.equal(x, y) for x, y in zip(r, want))
+
+
+# ------------------------------------------------------------------------------------------ prompts about the border of the two unit sizes
+@pytest.mark.parametrize("B,Hq,Hkv,n_q,n_kv,d", [(4, 8, 8, 1300, 1300, 64), (4, 8, 8, 1100, 1300, 128), (4, 16, 8, 260, 1300, 64), (4, 8, 8, 140, 1300, 128),
+                                                 (6, 8, 8, 128, 1024, 64), (5, 8, 8, 128, 1024, 64), (4, 8, 8, 1300, 700, 128), (9, 8, 8, 513, 513, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_prompt_weights(sdpa, B, Hq, Hkv, n_q, n_kv, d, causal):
+    import torch
+    q, k = rnd((B, Hq, n_q, d), 1), rnd((B, Hkv, n_kv, d), 2)
+    G, want = Hq // Hkv, torch.zeros((B, Hkv, n_kv), dtype=torch.float64, device="cuda")
+    lse = torch.zeros((B, Hq, n_q), device="cuda")
+    seen = torch.arange(n_kv, device="cuda") <= torch.arange(n_q, device="cuda")[:, None] + (n_kv - n_q)
+    for b in range(B):
+        s = q[b].double() @ k[b].repeat_interleave(G, 0).double().transpose(-1, -2) * d ** -0.5
+        if causal:
+            s.masked_fill_(~seen, -math.inf)
+        lse[b] = torch.logsumexp(s, -1).float()
+        w = torch.exp(s - lse[b, ..., None].double()).nan_to_num(nan=0.0)  # queries that see no key
+        want[b] = w.view(Hkv, G, n_q, n_kv).sum((1, 2))
+    acc = sdpa.fwd_acc(q, k, lse, causal=causal)
+    # scores of a few units, off by less than 2^-12; the sums by 2^-22 for each of their sqrt(n) steps
+    rel = 2.0 ** -12 + 2.0 ** -22 * math.sqrt(n_q * G)
+    assert ((acc.double() - want).abs() <= rel * want + n_q * G * 2.0 ** -126).all()
+    assert torch.equal(acc, sdpa.fwd_acc(q, k, lse, causal=causal))
