@@ -16,6 +16,9 @@
  * else SDPA_ERR_UNSUPPORTED.  Unlike sdpa_decode, lengths may be 0 here (an empty slot of a padded batch).
  * int32 and float arrays (lengths, LSE, weights, kept rows) need 4-byte alignment only.
  * batch * heads * rows of every array is at most 2^31 - 8192, batch and heads are at most 65535.
+ * Values may be of any finite size as long as scores, scale q . k, and for bf16 caches q . k itself are finite in 32 bits (scores
+ * times log2 e).  A key whose score is -inf weighs 0; a NaN or +inf score makes its query NaN.  In the 4-bit decode, elements of q
+ * below 2^-27 times their head's largest lose bits, and values are exact to bf16 beside rows up to 2^100 times as large.
  *
  * The 4-bit row.  The d channels form NG = d / 32 groups of 32.  Group g has a scale s and a minimum m,
  * both bf16, and a code c in 0 .. 15 for each channel, which stands for the number s c + m.
@@ -40,7 +43,8 @@ extern "C" {
  * t < n_new[b] (n_new NULL: all n_rows); kv_lens, n_new: int32 [batch] in device memory, 0 <= kv_lens[b],
  * 0 <= n_new[b] <= n_rows, kv_lens[b] + n_new[b] <= n_kv_cap (rows past the capacity are not written
  * and SDPA_ERR_DEVICE_BAD_LENGTH is recorded).  The lengths are not changed; other cache rows are
- * left as they were.
+ * left as they were.  Weights kept beside the cache are not touched: before rows are written where others were (a slot
+ * that starts again at length 0), zero the weights there (an eviction zeroes them past the rows that it keeps).
  * Per group: m = the smallest value, s = the smallest bf16 number not below (largest - m) / 15, and
  * c = (x - m) / s rounded to the nearest whole number, halves to the even one, from the exact quotient
  * (c = 0 where s = 0), so |x - (s c + m)| <= s / 2.  A group with a NaN or an infinity gets
@@ -67,14 +71,17 @@ SDPA_API int sdpa_kv4_load(const void* k_codes, const void* k_scales, const void
  *
  * Q [batch, heads_q, d], O [batch, heads_q, d] bf16; LSE [batch, heads_q] float or NULL.  Query head h reads
  * key/value head h / (heads_q / heads_kv).  Sequence b attends to cache rows 0 .. kv_lens[b] - 1
- * (0 <= kv_lens[b] <= n_kv_cap); other rows are never used.  kv_lens[b] == 0: O = 0, LSE = -inf.
+ * (0 <= kv_lens[b] <= n_kv_cap); other rows are never used.  kv_lens[b] == 0, or all scores -inf: O = 0, LSE = -inf,
+ * weights 0.
  * Keys and values enter as the numbers s c + m they stand for (not rounded to bf16 first).
  * acc_out [batch, heads_kv, n_kv_cap] float or NULL:
  *     acc_out[b, g, j] = acc[b, g, j] + sum over the query heads h of group g of exp(scale q_h . k_j - LSE_h)
  * for j < kv_lens[b]; entries at or past kv_lens[b] are left as they were.  acc may be acc_out (the usual
  * running sum) or NULL (zeros); acc without acc_out, or overlapping it in part, is SDPA_ERR_INVALID_ARG.
- * workspace: sdpa_decode_kv4_workspace_size bytes (with_acc: whether acc_out is given), scratch.  Calls that may run at
- * the same time (other streams, graphs replayed side by side) need one each.
+ * workspace: sdpa_decode_kv4_workspace_size bytes (with_acc: whether acc_out is given), scratch: a few MB, and with weights 4
+ * bytes for every query head and row of capacity (n_kv_cap, not the lengths: at d = 128 a cache row pair is 160 bytes, its group's
+ * scores 32 for 8 query heads).  Calls that may run at the same time (other streams, graphs replayed side by side) need
+ * one each.
  */
 SDPA_API size_t sdpa_decode_kv4_workspace_size(int batch, int heads_q, int heads_kv, int n_kv_cap, int d, int with_acc);
 SDPA_API int sdpa_decode_kv4(const void* Q, const void* k_codes, const void* k_scales, const void* v_codes,
@@ -96,7 +103,8 @@ SDPA_API int sdpa_decode_acc(const void* Q, const void* K, const void* V, const 
  *     acc_out[b, g, j] = acc[b, g, j] + sum over the heads h of group g and the queries i that see key j of
  *                        exp(scale q_hi . k_j - LSE_hi)
  * for j < n_kv.  Q [batch, heads_q, n_q, d], K [batch, heads_kv, n_kv, d] bf16; LSE [batch, heads_q, n_q] as
- * sdpa_fwd wrote it for the same scale and mask (a query with LSE = -inf or +inf adds nothing).  causal is
+ * sdpa_fwd wrote it for the same scale and mask (a query with LSE = -inf or +inf adds nothing where its scores are below
+ * +inf; a weight is as exact as the LSE's rounding, 2^-24 of it, allows).  causal is
  * bottom-right aligned, so the last n_q queries of a longer prompt may be given alone.  acc, acc_out
  * [batch, heads_kv, n_acc], n_acc >= n_kv (the decode cache's capacity); entries at or past n_kv are left
  * as they were; acc may be acc_out (not overlap it in part) or NULL (zeros).  n_q == 0 copies acc.

@@ -154,7 +154,8 @@ long long cache_score_stride(long long n_cap) { return (n_cap + 3) / 4 * 4; }
 // Query heads per unit of work: up to 8, or up to 16 where the group has more.
 int cache_unit_heads(int group) { return group > 8 ? 16 : 8; }
 
-// CTAs that share the work: what fits on the 148 SMs at once, as workspace sizes have to be known without a GPU.
+// CTAs that share the work: what fits on the 148 SMs of a B200 at once, as workspace sizes have to be known without a GPU.  No CTA
+// waits for another, so fewer SMs only take more than one wave.
 template <int D, bool KV4, bool WIDE>
 constexpr int kCacheCtas = 148 * sdpa::CacheCfg<D, KV4, WIDE>::MIN_BLOCKS;
 

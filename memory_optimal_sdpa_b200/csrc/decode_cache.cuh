@@ -4,33 +4,38 @@
 // The keys of all (sequence, key/value head, block of query heads) units, in blocks of 64 or 128, are one long
 // line of work that is cut evenly among as many CTAs as fit on the GPU at once: lengths differ, and a
 // wave that is not full costs as much as a full one (splits of 2048 keys 183 us, two, three, four lines' worth of CTAs 168,
-// 170, 173 us against 165 us for the case below).  A CTA's cut is one or more segments, each of one unit; a segment gives
+// 170, 173 us against 165 us for the case below when this was chosen).  A CTA's cut is one or more segments, each of one unit; a segment gives
 // a normalised partial output and a log-sum-exp (base 2, as a maximum and a sum) per query head.  Segment number unit + CTA is unique,
 // as both only grow along the line.  With weights the scores (base 2, fp32) are written too: a key's weight
 // needs the log-sum-exp over all of its unit's segments, and 4 bytes a score, written and read once, cost far less than
 // reading the keys again.  sdpa_cache_finish_kernel joins the segments and adds sum_h 2^(score_h - m_h) / l_h per key.
 //
-// What bounds it: HBM, if the arithmetic fits under it.  A 4-bit row pair of d = 128 is 160 bytes, 6.9 clocks of an
-// SM's share of HBM, in which 256 codes have to become operands.  So the codes never leave registers:
-// mma.sync takes its B operand from the registers they were unpacked in, where tcgen05 would need them
+// What bounds it: HBM, if the arithmetic fits under it.  A 4-bit row pair of d = 128 is 160 bytes, 6.4 clocks (at the 1.77 GHz
+// of the profile below) of an SM's share of HBM, in which 256 codes have to become operands.  So the codes never leave registers:
+// mma.sync takes its A operand from the registers they were unpacked in, where tcgen05 would need them
 // written to shared memory as 16-bit numbers and read back (512 + 512 bytes, 8 clocks).  Measured on this
 // part: m16n8k16 one per 2.1 clocks (one a key here), integer operations two warp instructions a clock, of which a key
-// needs nine, six of them for the codes.  64 x 64 heads over 8, cache 16384 (713 MB): 165 us, 4.3 TB/s; the split
-// kernel alone 147 us, 8.1 clocks a key at 2.4 of 4 instructions a clock, so the instructions bound it (without them, the
-// same loads 120 us), whether 8, 12 or 16 warps share the SM (166 / 165 / 172 us).  bf16, 4 x 32 heads over 8, 32768, with
-// weights (439 MB): 84 us, 5.2 TB/s, of which the finishing kernel 10.6 us (two keys a thread in place of its eight: 12).
+// needs nine, six of them for the codes.  64 x 64 heads over 8, cache 16384 (713 MB): 161-169 us, 4.2-4.4 TB/s.  The split
+// kernel alone, profiled: 152 us or 269000 clocks, 8.9 a key, in which it issues 19.7 instructions (2.35 a clock of the 4 there
+// are, 2.2 with its start and end), so the instructions bound it (without them the same loads take 120 us), whether 8, 12 or 16
+// warps share the SM (166 / 165 / 172 us when this was chosen).  bf16, 4 x 32 heads over 8, 32768, with
+// weights (439 MB): 84 us, 5.2 TB/s, of which the finishing kernel 9 us.  More than 8 query heads to a key/value head (WIDE: two
+// MMAs for each, 255 registers with 20 bytes spilled at d = 128, two CTAs an SM): 64 sequences of 8192 rows, d = 128, 8 key/value heads,
+// 8 / 12 / 16 / 20 heads each 146 / 208 / 208 / 386 us (20: two units, which read the cache twice), at d = 64 134 us for 12 and 16;
+// bf16 with weights, 16 such sequences, 112 / 120 / 126 / 212 us.
 //
 // Unpacking: (w & 0x000F000F) is, read as two fp16 numbers, c 2^-24 exactly (subnormal), and
 // (w & 0x00F000F0) 16 c 2^-24: one integer operation gives two operands.  The powers of two are put back
 // with the group scales.  For that Q enters as fp16, normalised by a power of two per head so that its
-// largest element is near 2^14 (the 8 significant bits of bf16 fit in fp16's 11; elements 2^-28 times the
-// largest and smaller lose bits, far below the rounding of the 32-bit sums).
+// largest element is near 2^14 (the 8 significant bits of bf16 fit in fp16's 11; elements 2^-27 times the
+// largest and smaller lose bits, far below the rounding of the 32-bit sums unless a key is as much larger there).
 //   scores   S[h, j] = sum_g s_jg (sum_{i in g} q_hi c_ji) + m_jg (sum_{i in g} q_hi)
 //   output   O[h, i] = sum_j (p_hj s_jg) c_ji + sum_j p_hj m_jg          (g the group of channel i)
 // p s is rounded to fp16, scaled by a power of two f that the scales of the tile set: 2^-3 <= s f < 2^11, so half a step is 2^-12 of
 // it (a sixteenth of the rounding of O to bf16) for p from 2^-11 on, and below that 2^-22 of s at most.  The sums with m and everything
 // else stay in fp32.  A tile whose scales leave that range moves f; one whose scales are too far apart for any f (an outlier
-// among the rows) is added up in fp32, as the other rows would lose their bits to it.
+// among the rows) is added up in fp32, as the other rows would lose their bits to it: 64 x 64 heads over 8, 8192 rows of normal
+// values 146 us; with a row 2^14 times as large among 8192 155 us, among 1024 185, among 128 452, in every tile 761 us.
 // bf16 caches use the same kernel with bf16 products; there p is split in two bf16 parts (its rounding to one
 // would cost as much again as that of O).
 // Both products put the cache on the MMA's side of 16 rows (keys, then channels) and the heads on its side of 8, so
@@ -71,7 +76,7 @@ struct CacheDecodeParams {
   int scale_exp;     // 2 where it is a quarter: log2 e takes the largest scales out of range
 };
 
-// WIDE: 9 to 16 query heads per CTA, else up to 8.  The MMA has 16 rows either way.
+// WIDE: 9 to 16 query heads per CTA, else up to 8.  Heads are on the MMA's side of 8, so WIDE takes two products for one.
 template <int D, bool KV4, bool WIDE>
 struct CacheCfg {
   static constexpr int WARPS = 4;
@@ -101,10 +106,10 @@ struct CacheLine {
   __device__ __forceinline__ static int blocks(const CacheDecodeParams& p, int b) {
     return (cache_len(p.kv_lens, b, p.n_cap) + p.block - 1) / p.block;
   }
-  // By a whole warp.
   __device__ __forceinline__ CacheLine(const CacheDecodeParams& p, long long total_) : total(total_) {
     n = (int)min((long long)p.n_cta, total);
   }
+  // By a whole warp.
   __device__ __forceinline__ CacheLine(const CacheDecodeParams& p, int lane) {
     int sum = 0;  // below 2^31: batch * heads * n_cap is
     for (int b = lane; b < p.B; b += 32) sum += blocks(p, b);

@@ -9,6 +9,10 @@
 // sdpa_evict_rows_kernel moves the rows; it reads and writes each kept row once (the bound: HBM).  Into another
 // cache all rows move at once; in place sdpa_evict_rows_in_place_kernel goes through a sequence's rows in order.  Both are
 // programmatic dependents of the selection and wait for it first (2 us of 67 for 16 x 8 heads, 8192 -> 2048 rows of 256 bytes).
+// A block picks its array's pointers from its parameters at run time, which puts those 120 bytes in local memory.
+// In place the rounds of a sequence and head run one after another in a block for each array and 64-byte slice of its rows.
+// Whole calls, in place and into another cache: 16 x 8 heads, d = 128, 4001-8192 -> 2048 rows bf16 87 and 69 us, 4 bits 42 and 36 us; 1 x 8 heads,
+// 32768 -> 4096 rows bf16 52 and 38 us, 4 bits 52 and 34 us; 1 x 8 heads, d = 64, 4096 -> 1024 rows bf16 20 and 15 us.
 #pragma once
 
 #include "kv4.cuh"

@@ -230,7 +230,7 @@ __device__ __forceinline__ void kv4_unpack(uint32_t codes, float (&code)[8]) {
   }
 }
 
-// Blocks of 128 threads at 64 registers.  4 x 8 heads, d = 128: append of 5001-8192 rows 51.7 us, load of 9001-16384 rows 45.3 us;
+// Blocks of 128 threads at 64 registers (append spills 52 bytes at that limit).  4 x 8 heads, d = 128: append of 5001-8192 rows 51.7 us, load of 9001-16384 rows 45.3 us;
 // 256 threads at 78 registers 57.2 and 47.0 us, at 64 registers 51.8 and 46.9 us, 128 threads at 72 and 56 registers 53.0
 // and 51.1 us (append), 64 threads 51.5 and 46.3 us.
 constexpr int KV4_THREADS = 128;

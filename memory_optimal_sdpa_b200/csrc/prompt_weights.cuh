@@ -22,7 +22,8 @@
 // four warps.  S^T stages: 512 / (128 MT) in TMEM, so the MMA runs ahead across units.  Query tile i of a CTA goes to the
 // groups of turn i mod TURNS (one group for each 128 keys), so that a stage always meets the same groups and they
 // wait for each of its phases in order: a parity cannot be mistaken for a later one.  At the end of a unit the group that had its last
-// tile collects the other turns' sums through shared memory (monotonic counters, two slots) and stores.
+// tile collects the other turns' sums through shared memory (monotonic counters, two slots) and stores.  640 threads leave 96 registers
+// each, at which MT = 2 spills 20 bytes.
 #pragma once
 
 #include "kv4.cuh"
