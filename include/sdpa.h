@@ -133,6 +133,7 @@ SDPA_API size_t sdpa_decode_workspace_size(int batch, int heads, int n_kv_cap, i
  * afterwards.  A length outside [1, n_kv_cap] is clamped on the device and
  * reported as SDPA_ERR_DEVICE_BAD_LENGTH by sdpa_get_last_device_error.
  * (A single query row sees every cached key, so causal masking does not apply.)
+ * A key whose score is -inf weighs 0; where all of them are, O = 0 and LSE = -inf.
  */
 SDPA_API int sdpa_decode(const void* Q, const void* K, const void* V, const int* kv_lens, void* O, float* LSE,
                 int batch, int heads, int n_kv_cap, int d_k, int d_v, float scale, void* workspace,

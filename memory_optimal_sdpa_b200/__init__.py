@@ -432,7 +432,7 @@ def _launch(where, dev, stream, *args):
 def kv4_append(cache, k, v, kv_lens, n_new=None, k_read=None, v_read=None, stream=None):
     """Quantise k, v [B,H,n_rows,d] bf16 into `cache`: row t of sequence b becomes cache row kv_lens[b] + t
     (t < n_new[b]; all rows without n_new).  kv_lens, n_new: int32 [B] on the device; kv_lens is not
-    changed.  k_read, v_read (both or neither, shapes of k, v) receive the values the cache now stands for."""
+    changed, nor are weights kept beside the cache (zero them where a slot starts again at length 0).  k_read, v_read (both or neither, shapes of k, v) receive the values the cache now stands for."""
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     B, H, n_cap, d = _kv4(cache)
