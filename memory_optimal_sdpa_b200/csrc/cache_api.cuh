@@ -240,8 +240,9 @@ int cache_decode(sdpa::CacheDecodeParams p, bool kv4, const void* Q, const int* 
   p.rows = (int)parts.heads;
   p.head_blocks = (p.group + p.rows - 1) / p.rows;
   p.score_stride = (int)cache_score_stride(n_cap);
-  p.scale_exp = std::fabs(scale) > 0x1p126f ? 2 : 0;
-  p.scale_log2 = (p.scale_exp ? 0.25f * scale : scale) * 1.4426950408889634f;
+  const float size = std::fabs(scale);
+  p.scale_exp = size > 0x1p126f ? 2 : size < 0x1p-100f ? -64 : 0;
+  p.scale_log2 = std::ldexp(scale, -p.scale_exp) * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.scores = acc_out ? p.part_o + (size_t)parts.rows * d : nullptr;  // 16-byte rows: the stride is a multiple of 4
   p.part_stat = (float2*)(p.part_o + (size_t)parts.rows * d + (acc_out ? (size_t)batch * heads_q * p.score_stride : 0));

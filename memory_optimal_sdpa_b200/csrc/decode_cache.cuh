@@ -72,8 +72,8 @@ struct CacheDecodeParams {
   int block;         // keys per block of work
   int n_cta;
   int score_stride;  // n_cap rounded up to 4
-  float scale_log2;  // scale log2 e, or a quarter of it
-  int scale_exp;     // 2 where it is a quarter: log2 e takes the largest scales out of range
+  float scale_log2;  // scale log2 e 2^-scale_exp
+  int scale_exp;     // 2 for the largest scales, which log2 e takes out of range, -64 for the least, whose bits it would round away
 };
 
 // WIDE: 9 to 16 query heads per CTA, else up to 8.  Heads are on the MMA's side of 8, so WIDE takes two products for one.

@@ -81,7 +81,8 @@ def make(sdpa, bits, B, Hkv, cap, d, lens, seed):
 # ------------------------------------------------------------------------------------------ sizes of q, of the scale and of the keys
 # The largest element of a head is in [2^e, 2^(e + 1)), scale is 2^a / 8, keys are times 2^b; e + a + b = 0 but for the last.
 EXPONENTS = [(127, -124, 0), (126, -123, 0), (125, -125, 0), (120, 0, -120), (127, -7, -120), (110, 10, -120), (124, -124, 0), (60, -60, 0),
-             (-60, 60, 0), (-100, 100, 0), (-120, 120, 0), (-126, 126, 0), (-126, 66, 60), (-20, -100, 120), (-126, 6, 120), (127, -127, -3)]
+             (-60, 60, 0), (-100, 100, 0), (-120, 120, 0), (-126, 126, 0), (-126, 66, 60), (-20, -100, 120), (-126, 6, 120), (127, -127, -3),
+             (103, -138, 35), (60, -140, 80), (127, -146, 19)]
 
 
 @pytest.mark.parametrize("d,G", [(64, 1), (128, 4), (128, 12)])
